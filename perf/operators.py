@@ -347,7 +347,7 @@ def work(case):
     if c["op"] == "write":
         return {"bytes": 4 * T * row + 4 * T, "flops": 0}
     if c["op"] == "accept":
-            depth = max(2, min(6, c["n"] // 4))
+        depth = max(2, min(6, c["n"] // 4))
         moved = 0.0  # rows that move, on average over the paths that prepare() draws
         for i in range(R):
             top = min(depth, max(1, int(new[i]) // 2))
