@@ -17,6 +17,17 @@ The names follow the C ABI:
     swiglu_check_device_status() -> raw status word (raises on timeout)
     swiglu_status_string(status) -> str
 
+and for serving steps that verify drafted tokens over a paged key/value cache
+(cache.py):
+
+    swiglu_cache_plan(ctx_lens, new_lens, pages_held, block_table, free_pages,
+                      page_size, max_tokens, parents=None) -> CachePlan
+    swiglu_cache_write(k, v, slots, k_cache, v_cache)
+    swiglu_tree_attention(q, k_cache, v_cache, block_table, ctx_lens,
+                          query_start, mask=None) -> out
+    swiglu_cache_accept(k_cache, v_cache, block_table, ctx_lens, paths,
+                        path_lens) -> new ctx_lens
+
 Y = SiLU(A x W1) (.) (A x W2) ("Tile-Level Activation Overlap for Efficient
 LLM Inference", Section 1 Introduction), BF16 in and out, FP32 accumulation.
 """
@@ -39,7 +50,9 @@ __all__ = [
     "swiglu_up_forward_fp8", "swiglu_down_packed_weight_bytes", "swiglu_pack_down_weights",
     "swiglu_pack_down_weights_nk", "swiglu_down_workspace_bytes", "swiglu_down_forward",
     "swiglu_mlp_workspace_bytes", "swiglu_mlp_forward", "swiglu_pack_weights_interleaved",
-    "swiglu_up_forward_interleaved", "EXPORTED_SYMBOLS",
+    "swiglu_up_forward_interleaved", "CachePlan", "swiglu_cache_plan", "swiglu_cache_write",
+    "swiglu_tree_attention_workspace_bytes", "swiglu_tree_attention", "swiglu_cache_accept",
+    "EXPORTED_SYMBOLS",
 ]
 
 SWIGLU_OK = 0
@@ -56,7 +69,8 @@ EXPORTED_SYMBOLS = (
     "swiglu_up_forward_fp8", "swiglu_down_packed_weight_bytes", "swiglu_pack_down_weights",
     "swiglu_pack_down_weights_nk", "swiglu_down_workspace_bytes", "swiglu_down_forward",
     "swiglu_mlp_workspace_bytes", "swiglu_mlp_forward", "swiglu_pack_weights_interleaved",
-    "swiglu_up_forward_interleaved",
+    "swiglu_up_forward_interleaved", "swiglu_cache_plan", "swiglu_cache_write",
+    "swiglu_tree_attention_workspace_bytes", "swiglu_tree_attention", "swiglu_cache_accept",
 )
 
 _lock = threading.Lock()
@@ -126,6 +140,20 @@ def load_library(path: str = LIB_PATH):
         lib.swiglu_pack_weights_interleaved.restype = ctypes.c_int
         lib.swiglu_up_forward_interleaved.argtypes = [vp, vp, vp, i64, i64, i64, vp, sz, vp]
         lib.swiglu_up_forward_interleaved.restype = ctypes.c_int
+        lib.swiglu_cache_plan.argtypes = [vp, vp, vp, vp, i64, i64, vp, i64, vp, i64, vp, i64, i64,
+                                          vp, vp, vp, vp, vp, vp, vp]
+        lib.swiglu_cache_plan.restype = ctypes.c_int
+        lib.swiglu_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, i64, i64, i64, vp, vp, vp,
+                                           i64, i64, vp]
+        lib.swiglu_cache_write.restype = ctypes.c_int
+        lib.swiglu_tree_attention_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        lib.swiglu_tree_attention_workspace_bytes.restype = sz
+        lib.swiglu_tree_attention.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, i64, i64, vp, vp,
+                                              vp, i64, f32, vp, i64, i64, i64, i64, vp, sz, vp]
+        lib.swiglu_tree_attention.restype = ctypes.c_int
+        lib.swiglu_cache_accept.argtypes = [vp, vp, i64, i64, i64, i64, i64, vp, i64, i64, vp, vp,
+                                            i64, vp, vp, vp]
+        lib.swiglu_cache_accept.restype = ctypes.c_int
         lib.swiglu_check_device_status.argtypes = [vp, u32p]
         lib.swiglu_check_device_status.restype = ctypes.c_int
         _lib = lib
@@ -536,3 +564,8 @@ def swiglu_check_device_status(stream=None) -> int:
         raise SwigluError(st, "device status word 0x%x" % raw.value)
     _check(st, "swiglu_check_device_status")
     return raw.value
+
+
+from .cache import (  # noqa: E402  (needs the helpers above)
+    CachePlan, swiglu_cache_accept, swiglu_cache_plan, swiglu_cache_write, swiglu_tree_attention,
+    swiglu_tree_attention_workspace_bytes)

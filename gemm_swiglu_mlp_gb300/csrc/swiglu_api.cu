@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache_kernels.cuh"
 #include "down_decode_kernel.cuh"
 #include "down_wide_kernel.cuh"
 #include "fused_up_kernel.cuh"
@@ -160,6 +161,9 @@ int device_setup(int *dev_out, DeviceState **st_out) {
                                  DecodeCfg<64>::SMEM_BYTES) != cudaSuccess ||
             cudaFuncSetAttribute(down_decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  DecodeCfg<128>::SMEM_BYTES) != cudaSuccess ||
+            // the cache plan's prefix sums at its largest number of requests
+            cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (2 * kPlanMaxRequests + 1) * 4) != cudaSuccess ||
             // its clusters of up to 16 CTAs (more than the portable 8)
             cudaFuncSetAttribute(down_decode_kernel<32>,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
@@ -588,7 +592,7 @@ void swiglu_test_set_fault_injection(int skip_first_fill) {
 }
 #endif
 
-int swiglu_version(void) { return (0 << 16) | 1; }
+int swiglu_version(void) { return (0 << 16) | 2; }
 
 const char *swiglu_status_string(int status) {
     switch (status) {
@@ -1410,3 +1414,5 @@ extern "C" int swiglu_test_busy_sms(int blocks, unsigned long long ns, void *str
     return SWIGLU_OK;
 }
 #endif
+
+#include "cache_api.cuh"

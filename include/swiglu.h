@@ -372,6 +372,135 @@ int swiglu_mlp_forward(const void *A, const void *Wpacked, const void *W3packed,
                        void *out, int64_t M, int64_t N, int64_t K,
                        void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention over a paged key/value cache, for serving steps that verify
+ * drafted tokens. The paper covers the gated MLP only; these entry points are
+ * this library's extension: the other half of a decoder layer's step.
+ *
+ * One step of R requests: request r has c_r cached tokens (its context) and
+ * n_r new ones - one token, a causal chain (a piece of a prompt), or a tree of
+ * drafted tokens. The new tokens of all requests lie one after the other,
+ * request r's in rows query_start[r] .. query_start[r + 1] - 1, T in all.
+ * New token i of request r is at position c_r + i of its cache.
+ *
+ * Cache: K and V each [num_pages][kv_heads][page_size][head_dim] BF16 (16-byte
+ * aligned). Position x of request r lies in page
+ * block_table[r * max_pages + x / page_size], row x % page_size; page *
+ * page_size + row is its slot. page_size is 16, 32, 64 or 128, head_dim 64 or
+ * 128, num_pages * page_size < 2^31 (other values: SWIGLU_ERR_UNSUPPORTED).
+ * All index arrays are device int32; nothing is read on the host, so every
+ * call may be captured into a CUDA graph and replayed with other lengths.
+ *
+ *     swiglu_cache_plan       lengths (and trees) -> pages, slots, masks
+ *     swiglu_cache_write      new K and V rows into the cache, by slot
+ *     swiglu_tree_attention   the new tokens' attention over the cache
+ *     swiglu_cache_accept     the verified path's rows behind the context
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Block tables, slot map, positions and tree masks of one step, in one launch.
+ *   ctx_lens, new_lens, pages_held  [requests]: c_r, n_r and the pages h_r that
+ *             request r holds (a negative value counts as 0, h_r is capped at
+ *             max_pages)
+ *   block_table  [requests, max_pages], updated in place: request r's entries
+ *             h_r .. need_r - 1 are written, need_r = max(h_r, min(max_pages,
+ *             ceil((c_r + n_r) / page_size))); the others stay
+ *   free_pages  [num_free]: pages to hand out, from entry *free_head (0 if
+ *             free_head is NULL) on, request by request; where the list ends
+ *             early, table entries and slots are -1
+ *   parents   [requests, tree_width] or NULL (tree_width 0): the parent of new
+ *             token i, an index among the request's new tokens smaller than i;
+ *             any other value (-1) hangs it on the context. new_lens above
+ *             tree_width count as tree_width. NULL: causal chains.
+ * Outputs:
+ *   query_start [requests + 1]: sums of new tokens
+ *   slots     [max_tokens]: each new token's slot; -1 without a page, and past
+ *             the last token
+ *   positions [max_tokens]: c_r + i, or c_r + the token's depth in its tree
+ *             (0 past the last token)
+ *   pages_held_out [requests]: h_r plus the pages got
+ *   counts    [3]: new tokens in all, new pages wanted, and the next step's
+ *             *free_head
+ *   mask      [max_tokens, ceil(tree_width / 64)] 64-bit words (only with
+ *             parents; else NULL): bit j of token i is set if j is i or an
+ *             ancestor of i; 0 past the last token
+ * Tokens past max_tokens get no outputs (counts[0] tells). Outputs must not
+ * overlap each other or the inputs. requests <= 16384; requests = 0 is valid.
+ * Errors: SWIGLU_ERR_INVALID_ARG, SWIGLU_ERR_UNSUPPORTED, SWIGLU_ERR_CUDA.
+ */
+int swiglu_cache_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *pages_held,
+                      int32_t *block_table, int64_t requests, int64_t max_pages,
+                      const int32_t *free_pages, int64_t num_free, const int32_t *free_head,
+                      int64_t page_size, const int32_t *parents, int64_t tree_width,
+                      int64_t max_tokens, int32_t *query_start, int32_t *slots,
+                      int32_t *positions, int32_t *pages_held_out, int32_t *counts,
+                      int64_t *mask, void *stream);
+
+/*
+ * Rows of K and V [tokens, kv_heads, head_dim] into the cache: row t, head h
+ * goes to slot slots[t]. Rows whose slot is negative or >= num_pages *
+ * page_size are dropped; two rows with one slot leave either. Bit-exact copy.
+ *   k, v      device BF16, strides in elements (multiples of 8; the last
+ *             dimension contiguous; 16-byte aligned), e.g. slices of a fused
+ *             projection's output
+ * K, V and slots must not overlap the caches. tokens = 0 is valid.
+ */
+int swiglu_cache_write(const void *k, const void *v, int64_t tokens, int64_t kv_heads,
+                       int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
+                       int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots,
+                       void *k_cache, void *v_cache, int64_t num_pages, int64_t page_size,
+                       void *stream);
+
+/* Workspace bytes of swiglu_tree_attention on the current device (0: none). */
+size_t swiglu_tree_attention_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                                             int64_t head_dim);
+
+/*
+ * out[t, h] = sum_x p_x v_x / sum_x p_x, p_x = exp(scale * q[t, h] . k_x - max),
+ * over the positions x that new token t (place i of request r) sees: the
+ * context, x < c_r, and x = c_r + j for every new token j < n_r of the request
+ * whose bit is set in mask[t, j / 64] (bit j % 64; bits past mask_words words
+ * count as 0). mask NULL (mask_words 0): j <= i, a causal chain. A token that
+ * sees nothing, or whose scores are all -inf, gets zeros; values at positions
+ * that a token does not see (also NaN or Inf) do not reach its output. Rows of
+ * `out` past query_start[requests] are set to zero.
+ *   q         device BF16 [tokens, q_heads, head_dim], strides in elements
+ *             (multiples of 8), 16-byte aligned; q_heads % kv_heads == 0, query
+ *             head h reads kv head h / (q_heads / kv_heads)
+ *   out       device BF16 [tokens, q_heads, head_dim] contiguous
+ *   scale     finite; 1 / sqrt(head_dim) as a rule
+ *   workspace as swiglu_up_forward, sized by
+ *             swiglu_tree_attention_workspace_bytes
+ * Sums and softmax statistics are FP32, the result is rounded once to BF16.
+ * query_start must not fall; positions past max_pages * page_size are not
+ * seen; a table entry outside the cache is never followed out of it.
+ * Errors: SWIGLU_ERR_INVALID_ARG, SWIGLU_ERR_UNSUPPORTED, SWIGLU_ERR_CUDA;
+ * device-side timeouts by swiglu_check_device_status.
+ */
+int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                          const void *k_cache, const void *v_cache, int64_t num_pages,
+                          int64_t page_size, const int32_t *block_table, int64_t requests,
+                          int64_t max_pages, const int32_t *ctx_lens, const int32_t *query_start,
+                          const int64_t *mask, int64_t mask_words, float scale, void *out,
+                          int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * After verification: in every layer's cache, row c_r + i of request r takes
+ * the value that row c_r + paths[r, i] had before the call, i < path_lens[r],
+ * and ctx_out[r] = c_r + path_lens[r].
+ *   k_cache, v_cache  [layers, num_pages, kv_heads, page_size, head_dim]
+ *   paths     [requests, path_width]: indices among the request's new tokens,
+ *             strictly increasing (the accepted path from the root on);
+ *             path_lens outside 0 .. path_width are capped
+ * A row without a valid page is not moved. ctx_out must not overlap an input.
+ */
+int swiglu_cache_accept(void *k_cache, void *v_cache, int64_t layers, int64_t num_pages,
+                        int64_t kv_heads, int64_t page_size, int64_t head_dim,
+                        const int32_t *block_table, int64_t requests, int64_t max_pages,
+                        const int32_t *ctx_lens, const int32_t *paths, int64_t path_width,
+                        const int32_t *path_lens, int32_t *ctx_out, void *stream);
+
 /*
  * Synchronizes `stream`, then reads and clears the current device's status
  * word. Every wait inside the kernels is bounded (about a second); a kernel
