@@ -303,7 +303,7 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     CacheShape shape;
     const int c = cache_shape(num_pages, kv_heads, page_size, head_dim, &shape);
     if (c != SWIGLU_OK) return c;
-    if (q_heads % kv_heads != 0 || !(scale - scale == 0.f)) return SWIGLU_ERR_INVALID_ARG;
+    if (q_heads % kv_heads != 0 || !(scale > 0.f) || !(scale - scale == 0.f)) return SWIGLU_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !query_start || (tokens > 0 && (!q || !out)) ||
         (requests > 0 && (!block_table || !ctx_lens)))
         return SWIGLU_ERR_INVALID_ARG;

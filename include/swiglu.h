@@ -468,7 +468,7 @@ size_t swiglu_tree_attention_workspace_bytes(int64_t tokens, int64_t q_heads, in
  *             (multiples of 8), 16-byte aligned; q_heads % kv_heads == 0, query
  *             head h reads kv head h / (q_heads / kv_heads)
  *   out       device BF16 [tokens, q_heads, head_dim] contiguous
- *   scale     finite; 1 / sqrt(head_dim) as a rule
+ *   scale     finite and > 0; 1 / sqrt(head_dim) as a rule
  *   workspace as swiglu_up_forward, sized by
  *             swiglu_tree_attention_workspace_bytes
  * Sums and softmax statistics are FP32, the result is rounded once to BF16.
