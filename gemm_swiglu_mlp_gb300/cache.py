@@ -22,8 +22,12 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_check, _default_workspace, _OnDevice, _out_tensor, _require_bf16_cuda,
-               _stream_handle, load_library)
+from . import (SWIGLU_ERR_INVALID_ARG, SwigluError, _check, _OnDevice, _out_tensor,
+               _require_bf16_cuda, _stream_handle, load_library)
+
+# (device index, stream handle) -> uint8 tensor; apart from the other entry
+# points' workspaces, whose counters have to stay as they are between calls
+_workspaces = {}
 
 
 class CachePlan(NamedTuple):
@@ -171,6 +175,24 @@ def swiglu_tree_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: i
         int(tokens), int(q_heads), int(kv_heads), int(head_dim)))
 
 
+def _workspace(device, nbytes: int, stream) -> torch.Tensor:
+    """One attention workspace per (device, stream), grown on demand."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    key = (device.index, int(s.cuda_stream))
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        if torch.cuda.is_current_stream_capturing():
+            # an allocation made during capture belongs to the graph's pool
+            raise SwigluError(SWIGLU_ERR_INVALID_ARG,
+                              "this call needs a workspace of %d bytes: allocate it before "
+                              "capturing (swiglu_tree_attention_workspace_bytes) and pass "
+                              "workspace=" % nbytes)
+        with torch.cuda.stream(s):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _workspaces[key] = ws
+    return ws
+
+
 def swiglu_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                           block_table: torch.Tensor, ctx_lens: torch.Tensor,
                           query_start: torch.Tensor, mask: torch.Tensor = None,
@@ -204,7 +226,7 @@ def swiglu_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         ws_ptr, ws_bytes = None, 0
         if need:
             if workspace is None:
-                workspace = _default_workspace(dev, need, stream)
+                workspace = _workspace(dev, need, stream)
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         _check(lib.swiglu_tree_attention(
             q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,

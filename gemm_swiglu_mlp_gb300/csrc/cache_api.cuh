@@ -62,6 +62,72 @@ int launch_overlapped(void (*kernel)(Args), dim3 grid, unsigned threads, size_t 
     return SWIGLU_OK;
 }
 
+// Tiles a block takes at least, and the tokens up to which a row tile's
+// queries are fetched token by token (a box of the whole tile reads 128 rows).
+constexpr int kTreeMinUnits = 2;
+constexpr int kTreeQOne = 4;
+
+// Workspace of one attention call: which items go on in another block, and
+// two partial results a block (of the item it takes over and of the one it
+// leaves).
+struct TreeWorkspace {
+    int rows;   // of one partial result
+    size_t stats, partial, bytes;
+};
+TreeWorkspace tree_workspace(int64_t tokens, int group, int head_dim, int sms) {
+    TreeWorkspace w;
+    w.rows = tokens <= kTreeTile / group ? 128 : 256;
+    const size_t parts = static_cast<size_t>(2) * sms * w.rows;
+    w.stats = static_cast<size_t>(round_up(16 * int64_t(sms), 256));
+    w.partial = w.stats + parts * sizeof(float2);
+    w.bytes = w.partial + parts * head_dim * sizeof(float);
+    return w;
+}
+
+// 3-D tensor map over BF16 [d2][d1][d0] with strides s1 and s2 (elements) and
+// a 128-byte-swizzled box of 64 x b1 x b2.
+bool encode_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
+               uint64_t s1, uint64_t s2, uint32_t b1, uint32_t b2) {
+    EncodeTiledFn enc = get_encode();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {d0, d1, d2};
+    const cuuint64_t strides[2] = {2 * s1, 2 * s2};
+    const cuuint32_t box[3] = {64, b1, b2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The attention kernel, one block per SM, and the sums of shared items.
+template <int D>
+int tree_launch(const CUtensorMap &tmQ, const CUtensorMap &tmQ1, const CUtensorMap &tmK,
+                const CUtensorMap &tmV, const TreeAttnArgs &a, int sms, void *stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(sms));
+    cfg.blockDim = dim3(kTreeThreads);
+    cfg.dynamicSmemBytes = TreeCfg<D>::SMEM_BYTES;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, tree_attention_kernel<D>, tmQ, tmQ1, tmK, tmV, a);
+    if (err == cudaSuccess) {
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * sms));
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.dynamicSmemBytes = 0;
+        err = cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a, sms);
+    }
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        return SWIGLU_ERR_CUDA;
+    }
+    return SWIGLU_OK;
+}
+
 // Bytes from the first to the last element of a [tokens, heads, head_dim]
 // BF16 view with the given strides (in elements, not negative).
 size_t rows_extent(int64_t tokens, int64_t heads, int64_t head_dim, int64_t tok, int64_t head) {
@@ -286,8 +352,11 @@ int swiglu_cache_accept(void *k_cache, void *v_cache, int64_t layers, int64_t nu
 
 size_t swiglu_tree_attention_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads,
                                              int64_t head_dim) {
-    (void)tokens, (void)q_heads, (void)kv_heads, (void)head_dim;
-    return 0;
+    if (tokens < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 ||
+        q_heads / kv_heads > kTreeTile || (head_dim != 64 && head_dim != 128))
+        return 0;
+    return tree_workspace(tokens, static_cast<int>(q_heads / kv_heads),
+                          static_cast<int>(head_dim), current_sm_count()).bytes;
 }
 
 int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -311,10 +380,14 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
         !aligned4(block_table) || !aligned4(ctx_lens) || !aligned4(query_start) ||
         !aligned8(mask) || !strides_ok(q_token_stride, q_head_stride))
         return SWIGLU_ERR_INVALID_ARG;
-    if (tokens >= kMaxI32 || q_heads > 65535 || tokens * q_heads >= kMaxI32 ||
-        requests >= kMaxI32 || max_pages >= (kMaxI32 >> shape.page_shift) ||
-        mask_words > (1 << 20))
+    const int64_t group = q_heads / kv_heads;
+    if (tokens >= kMaxI32 / 2 || q_heads > 65535 || tokens * q_heads >= kMaxI32 ||
+        requests >= kMaxI32 || max_pages >= (kMaxI32 / 2 >> shape.page_shift) ||
+        mask_words > (1 << 20) || group > kTreeTile)
         return SWIGLU_ERR_UNSUPPORTED;
+    // a tensor map's strides step over whole rows
+    if ((tokens > 1 && q_token_stride < head_dim) || (q_heads > 1 && q_head_stride < head_dim))
+        return SWIGLU_ERR_INVALID_ARG;
     if (tokens > 0) {
         const size_t obytes = static_cast<size_t>(tokens) * q_heads * head_dim * 2;
         if (overlaps(out, obytes, q,
@@ -323,36 +396,64 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
             overlaps(out, obytes, v_cache, shape.layer_bytes))
             return SWIGLU_ERR_INVALID_ARG;
     }
-    (void)workspace, (void)workspace_bytes;
     int dev;
     DeviceState *st;
     const int s = device_setup(&dev, &st);
     if (s != SWIGLU_OK) return s;
     if (tokens == 0) return SWIGLU_OK;
+    const TreeWorkspace ws = tree_workspace(tokens, static_cast<int>(group),
+                                            static_cast<int>(head_dim), st->sm_count);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < ws.bytes)
+        return SWIGLU_ERR_INVALID_ARG;
+    if (overlaps(workspace, ws.bytes, out,
+                 static_cast<size_t>(tokens) * q_heads * head_dim * 2) ||
+        overlaps(workspace, ws.bytes, q,
+                 rows_extent(tokens, q_heads, head_dim, q_token_stride, q_head_stride)) ||
+        overlaps(workspace, ws.bytes, k_cache, shape.layer_bytes) ||
+        overlaps(workspace, ws.bytes, v_cache, shape.layer_bytes))
+        return SWIGLU_ERR_INVALID_ARG;
     TreeAttnArgs a{};
-    a.q = static_cast<const uint16_t *>(q);
-    a.k_cache = static_cast<const uint16_t *>(k_cache);
-    a.v_cache = static_cast<const uint16_t *>(v_cache);
+    a.geom.requests = static_cast<int>(requests);
+    a.geom.tokens = static_cast<int>(tokens);
+    a.geom.kv_heads = static_cast<int>(kv_heads);
+    a.geom.group = static_cast<int>(group);
+    a.geom.tpt = kTreeTile / static_cast<int>(group);
+    a.geom.causal = mask == nullptr;
+    a.geom.max_rows = static_cast<int>(max_pages << shape.page_shift);
     a.table = block_table;
     a.ctx_lens = ctx_lens;
     a.query_start = query_start;
     a.mask = reinterpret_cast<const unsigned long long *>(mask);
+    a.v_cache = static_cast<const uint16_t *>(v_cache);
     a.out = static_cast<uint16_t *>(out);
-    a.q_tok = q_token_stride;
-    a.q_head = q_head_stride;
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    a.chains = reinterpret_cast<int4 *>(base);
+    a.stats = reinterpret_cast<float2 *>(base + ws.stats);
+    a.partial = reinterpret_cast<float *>(base + ws.partial);
     a.max_pages = max_pages;
-    a.num_pages = num_pages;
-    a.scale = scale;
-    a.tokens = static_cast<int>(tokens);
-    a.requests = static_cast<int>(requests);
+    a.scale_log2 = scale * 1.4426950408889634f;   // log2(e)
     a.q_heads = static_cast<int>(q_heads);
-    a.kv_heads = static_cast<int>(kv_heads);
+    a.num_pages = static_cast<int>(num_pages);
     a.page_shift = shape.page_shift;
     a.mask_words = static_cast<int>(mask_words);
-    const int64_t blocks = (tokens * q_heads + kRowAttnThreads / 32 - 1) / (kRowAttnThreads / 32);
-    return launch_overlapped(head_dim == 64 ? tree_attention_rows_kernel<64>
-                                            : tree_attention_rows_kernel<128>,
-                             dim3(static_cast<unsigned>(blocks)), kRowAttnThreads, 0, stream, a);
+    a.part_rows = ws.rows;
+    a.min_units = kTreeMinUnits;
+    a.q_one = kTreeQOne;
+    const uint64_t pages_heads = static_cast<uint64_t>(num_pages) * static_cast<uint64_t>(kv_heads);
+    CUtensorMap tmQ, tmQ1, tmK, tmV;
+    const uint64_t D = static_cast<uint64_t>(head_dim);
+    const uint64_t qh = q_heads > 1 ? q_head_stride : D, qt = tokens > 1 ? q_token_stride : D;
+    if (!encode_3d(&tmQ, q, D, q_heads, tokens, qh, qt, static_cast<uint32_t>(group),
+                   static_cast<uint32_t>(a.geom.tpt)) ||
+        !encode_3d(&tmQ1, q, D, q_heads, tokens, qh, qt, static_cast<uint32_t>(group), 1) ||
+        !encode_3d(&tmK, k_cache, D, page_size, pages_heads, D, D * page_size,
+                   static_cast<uint32_t>(page_size), 1) ||
+        !encode_3d(&tmV, v_cache, D, page_size, pages_heads, D, D * page_size,
+                   static_cast<uint32_t>(page_size), 1))
+        return SWIGLU_ERR_CUDA;
+    return head_dim == 64 ? tree_launch<64>(tmQ, tmQ1, tmK, tmV, a, st->sm_count, stream)
+                          : tree_launch<128>(tmQ, tmQ1, tmK, tmV, a, st->sm_count, stream);
 }
 
 }  // extern "C"

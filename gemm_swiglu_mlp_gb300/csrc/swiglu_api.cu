@@ -15,6 +15,7 @@
 #include "fused_up_kernel.cuh"
 #include "fused_up_pair_kernel.cuh"
 #include "pack_kernel.cuh"
+#include "tree_attention_kernel.cuh"
 #include "swiglu.h"
 
 namespace swiglu {
@@ -164,6 +165,12 @@ int device_setup(int *dev_out, DeviceState **st_out) {
             // the cache plan's prefix sums at its largest number of requests
             cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (2 * kPlanMaxRequests + 1) * 4) != cudaSuccess ||
+            cudaFuncSetAttribute(tree_attention_kernel<64>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 TreeCfg<64>::SMEM_BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(tree_attention_kernel<128>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 TreeCfg<128>::SMEM_BYTES) != cudaSuccess ||
             // its clusters of up to 16 CTAs (more than the portable 8)
             cudaFuncSetAttribute(down_decode_kernel<32>,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||

@@ -466,11 +466,14 @@ size_t swiglu_tree_attention_workspace_bytes(int64_t tokens, int64_t q_heads, in
  * `out` past query_start[requests] are set to zero.
  *   q         device BF16 [tokens, q_heads, head_dim], strides in elements
  *             (multiples of 8), 16-byte aligned; q_heads % kv_heads == 0, query
- *             head h reads kv head h / (q_heads / kv_heads)
+ *             head h reads kv head h / (q_heads / kv_heads), at most 128 per kv head;
+ *             the strides are at least head_dim
  *   out       device BF16 [tokens, q_heads, head_dim] contiguous
  *   scale     finite and > 0; 1 / sqrt(head_dim) as a rule
- *   workspace as swiglu_up_forward, sized by
- *             swiglu_tree_attention_workspace_bytes
+ *   workspace device scratch of swiglu_tree_attention_workspace_bytes, 256-byte
+ *             aligned, any content; every call overwrites it, so calls that run
+ *             at the same time need their own, and it is not the workspace of
+ *             the other entry points (whose counters must stay)
  * Sums and softmax statistics are FP32, the result is rounded once to BF16.
  * query_start must not fall; positions past max_pages * page_size are not
  * seen; a table entry outside the cache is never followed out of it.

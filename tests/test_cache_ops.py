@@ -103,7 +103,8 @@ def test_attention_refusals(lib):
                 dict(scale=-1.0), dict(out=a[0]),
                 dict(out=a[1]), dict(out=a[2])):
         assert call(**bad) == 1, bad
-    for bad in (dict(D=96), dict(P=20), dict(T=1 << 31), dict(mp=1 << 31), dict(words=1 << 21)):
+    for bad in (dict(D=96), dict(P=20), dict(T=1 << 31), dict(mp=1 << 31), dict(words=1 << 21),
+                dict(Hq=258)):
         assert call(**bad) == 2, bad
 
 
