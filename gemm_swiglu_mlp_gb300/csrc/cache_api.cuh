@@ -64,7 +64,7 @@ int launch_overlapped(void (*kernel)(Args), dim3 grid, unsigned threads, size_t 
 
 // Tiles a block takes at least, and the tokens up to which a row tile's
 // queries are fetched token by token (a box of the whole tile reads 128 rows).
-constexpr int kTreeMinUnits = 2;
+constexpr int kTreeMinUnits = 1;
 constexpr int kTreeQOne = 4;
 
 // Workspace of one attention call: which items go on in another block, and

@@ -81,6 +81,34 @@ SWIGLU_HD long long tree_head_units(const TreeGeom &g, const TreeReq &q) {
     return u;
 }
 
+// a / b for a >= 0, b > 0: nearly every a fits 32 bits, whose division is
+// several times cheaper on the GPU.
+SWIGLU_HD long long tree_div(long long a, int b) {
+    if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// The line of `total` units cut for `blocks` blocks: the first `more` of them
+// take one unit above `each`.
+struct TreeCut {
+    long long each;
+    int more;
+};
+SWIGLU_HD TreeCut tree_cut(long long total, int blocks) {
+    TreeCut c;
+    c.each = tree_div(total, blocks);
+    c.more = static_cast<int>(total - c.each * blocks);
+    return c;
+}
+SWIGLU_HD long long tree_block_begin(const TreeCut &c, int block) {
+    return c.each * block + tree_min(block, c.more);
+}
+// Block that does unit u (each >= 1).
+SWIGLU_HD int tree_block_of(const TreeCut &c, long long u) {
+    const long long fat = (c.each + 1) * c.more;
+    return static_cast<int>(u < fat ? u / (c.each + 1) : c.more + (u - fat) / c.each);
+}
+
 // Where a block begins: `tile` of item (r, h, item), `units` tiles to do.
 struct TreeStart {
     int r, h, item, tile;
@@ -90,7 +118,9 @@ struct TreeStart {
 // The place `rem` units into request r.
 SWIGLU_HD void tree_locate(const TreeGeom &g, const TreeReq &q, long long rem, TreeStart *s) {
     const long long per_head = tree_head_units(g, q);
-    s->h = static_cast<int>(rem / per_head);
+    s->h = static_cast<int>((rem >> 32) == 0 && (per_head >> 32) == 0
+                                ? static_cast<uint32_t>(rem) / static_cast<uint32_t>(per_head)
+                                : rem / per_head);
     rem -= s->h * per_head;
     int item = 0;
     while (true) {
@@ -103,38 +133,58 @@ SWIGLU_HD void tree_locate(const TreeGeom &g, const TreeReq &q, long long rem, T
     s->tile = static_cast<int>(rem);
 }
 
-// Block that does unit u.
-SWIGLU_HD int tree_block_of(long long u, long long total, int blocks) {
-    return static_cast<int>(((u + 1) * blocks + total - 1) / total) - 1;
-}
-SWIGLU_HD long long tree_block_begin(int c, long long total, int blocks) {
-    return total * c / blocks;
-}
+// One softmax group's part in an entry (below): a row tile and the tiles
+// first, first + stride, .. (< end) of its item.
+struct TreePart {
+    int r, h;         // request, kv head
+    int tok;          // first token of the row tile (row of q)
+    int place;        // its place among the request's new tokens
+    int ntok;         // tokens of the row tile
+    int ctx, len;     // of the request; positions of the item
+    int first, stride, end;
+    int flags;
 
-// The items of one block in order, and the steps of each. An item of one row
-// tile (`pair` false) is worked on by both softmax groups, group s taking the
-// tiles tb + s, tb + s + 2, ..: two tiles a step. An item of two row tiles
-// gives each group one of them: both see every tile, one a step.
+    SWIGLU_HD bool used() const { return first < end; }
+    SWIGLU_HD bool active(int step) const { return first + step * stride < end; }
+    SWIGLU_HD int tile(int step) const { return first + step * stride; }
+    SWIGLU_HD bool last(int step) const { return first + (step + 1) * stride >= end; }
+    // a tile with positions that need a look: new tokens, or past the end
+    SWIGLU_HD bool edge(int t) const { return (t + 1) * kTreeTile > tree_min(ctx, len); }
+};
+enum : int {
+    kPartWhole = 1,    // this block does the whole item
+    kPartBegins = 2,   // the item begins in this block
+    kPartSecond = 4,   // the item's second row tile
+    kPartShared = 8,   // the other group works on the same row tile (kTreeSplit)
+};
+
+// What both groups do next. kTreeSplit: an item of one row tile, the groups
+// take its even and odd tiles and merge their results. kTreePair: an item of
+// two row tiles, one a group, over the same tiles. kTreeDuo: two short items
+// of one row tile each, one a group; while one group's softmax or result runs,
+// the tensor cores work for the other (kTreeDuoTiles: 608 one-tile items on
+// 152 blocks, see the kernel).
+enum : int { kTreeSplit = 0, kTreePair = 1, kTreeDuo = 2 };
+constexpr int kTreeDuoTiles = 4;
+struct TreeEntry {
+    TreePart part[2];
+    int kind;
+    int steps;        // 0: nothing left
+    SWIGLU_HD bool two_q() const { return kind != kTreeSplit; }    // a Q tile a group
+    SWIGLU_HD bool two_kv() const { return kind != kTreePair; }    // K and V tiles a group
+};
+
+// The items of one block in order.
 struct TreeWalk {
     TreeReq q;
-    int r, h, item;
-    int tokens;        // of the item
-    int len;           // positions of the item
-    int tiles;         // of the item
-    int tb, te;        // this block's tiles of it
-    long long left;    // units left, this item's included
-    int seq;           // items before this one in this block
-    int step, steps;
-    bool pair;
+    int r, h, item, items;
+    int tokens, len, tiles;   // of the item
+    int tb, te;               // this block's tiles of it
+    long long left;           // units left, this item's included
 
     SWIGLU_HD bool valid() const { return left > 0; }
+    SWIGLU_HD bool pair(const TreeGeom &g) const { return tokens > g.tpt; }
     SWIGLU_HD int item_token0(const TreeGeom &g) const { return item * 2 * g.tpt; }
-    SWIGLU_HD bool active(int s) const { return pair || tb + 2 * step + s < te; }
-    SWIGLU_HD int tile(int s) const { return pair ? tb + step : tb + 2 * step + s; }
-    SWIGLU_HD bool last_of(int s) const { return pair ? step + 1 == steps : tb + 2 * step + s + 2 >= te; }
-    SWIGLU_HD bool uses(int s) const { return pair || s == 0 || te - tb > 1; }
-    // a tile with positions that need a look: new tokens, or past the end
-    SWIGLU_HD bool edge(int t) const { return (t + 1) * kTreeTile > q.ctx || (t + 1) * kTreeTile > len; }
 
     SWIGLU_HD void set_item(const TreeGeom &g, int from) {
         tokens = tree_item_tokens(g, q, item);
@@ -142,9 +192,6 @@ struct TreeWalk {
         tiles = (len + kTreeTile - 1) / kTreeTile;
         tb = from;
         te = static_cast<int>(left < tiles - from ? from + left : tiles);
-        pair = tokens > g.tpt;
-        step = 0;
-        steps = pair ? te - tb : (te - tb + 1) / 2;
     }
     template <typename Load>   // Load(r) -> TreeReq
     SWIGLU_HD void begin(const TreeGeom &g, const TreeStart &s, Load load) {
@@ -152,30 +199,81 @@ struct TreeWalk {
         h = s.h;
         item = s.item;
         left = s.units;
-        seq = 0;
         if (left <= 0) return;
         q = load(r);
+        items = tree_items(g, q);
         set_item(g, s.tile);
     }
     // The next item, or left = 0.
     template <typename Load>
-    SWIGLU_HD void next_item(const TreeGeom &g, Load load) {
+    SWIGLU_HD void next(const TreeGeom &g, Load load) {
         left -= te - tb;
-        ++seq;
         if (left <= 0) return;
-        if (++item == tree_items(g, q)) {
+        if (++item == items) {
             item = 0;
             if (++h == g.kv_heads) {
                 h = 0;
                 do q = load(++r);
                 while (q.n == 0);
+                items = tree_items(g, q);
             }
         }
         set_item(g, 0);
     }
+    SWIGLU_HD TreePart part(const TreeGeom &g, int rt, int first, int stride) const {
+        TreePart p;
+        p.r = r;
+        p.h = h;
+        p.place = item_token0(g) + rt * g.tpt;
+        p.tok = q.t0 + p.place;
+        p.ntok = tree_min(g.tpt, tokens - rt * g.tpt);
+        p.ctx = q.ctx;
+        p.len = len;
+        p.first = first;
+        p.stride = stride;
+        p.end = te;
+        p.flags = (tb == 0 && te == tiles ? kPartWhole : 0) | (tb == 0 ? kPartBegins : 0) |
+                  (rt ? kPartSecond : 0);
+        return p;
+    }
+    // The next entry; moves on past its items. steps = 0 at the end.
     template <typename Load>
-    SWIGLU_HD void next_step(const TreeGeom &g, Load load) {
-        if (++step == steps) next_item(g, load);
+    SWIGLU_HD TreeEntry entry(const TreeGeom &g, Load load) {
+        TreeEntry e;
+        e.kind = kTreeSplit;
+        e.steps = 0;
+        if (!valid()) return e;
+        const int mine = te - tb;
+        if (pair(g)) {
+            e.kind = kTreePair;
+            e.steps = mine;
+            e.part[0] = part(g, 0, tb, 1);
+            e.part[1] = part(g, 1, tb, 1);
+            next(g, load);
+            return e;
+        }
+        if (mine <= kTreeDuoTiles && left > mine) {
+            e.part[0] = part(g, 0, tb, 1);
+            next(g, load);
+            if (!pair(g) && te - tb <= kTreeDuoTiles) {
+                e.kind = kTreeDuo;
+                e.part[1] = part(g, 0, tb, 1);
+                e.steps = tree_max(mine, te - tb);
+                next(g, load);
+                return e;
+            }
+        } else {
+            e.part[0] = part(g, 0, tb, 1);
+            next(g, load);
+        }
+        e.part[1] = e.part[0];
+        e.part[1].first += 1;
+        for (int s = 0; s < 2; ++s) {
+            e.part[s].stride = 2;
+            e.part[s].flags |= kPartShared;
+        }
+        e.steps = (mine + 1) / 2;
+        return e;
     }
 };
 

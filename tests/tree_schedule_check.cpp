@@ -51,12 +51,12 @@ int main(int argc, char **argv) {
         std::map<std::tuple<int, int, int>, int> done;   // tiles done so far of an item
         std::map<std::tuple<int, int, int>, std::pair<int, int>> by;   // first and last block
         std::map<std::tuple<int, int, int>, int> says;   // last block as the first one says
+        const TreeCut cut = tree_cut(total, blocks);
         long long units = 0;
         for (int c = 0; c < blocks; ++c) {
-            const long long u0 = tree_block_begin(c, total, blocks);
-            const long long u1 = tree_block_begin(c + 1, total, blocks);
-            CHECK(u1 > u0);
-            CHECK(tree_block_of(u0, total, blocks) == c && tree_block_of(u1 - 1, total, blocks) == c);
+            const long long u0 = tree_block_begin(cut, c), u1 = tree_block_begin(cut, c + 1);
+            CHECK(u1 > u0 && u1 <= total);
+            CHECK(tree_block_of(cut, u0) == c && tree_block_of(cut, u1 - 1) == c);
             int r = 0;
             while (r + 1 < g.requests && before[r + 1] <= u0) ++r;
             while (load(r).n == 0) --r;
@@ -65,42 +65,60 @@ int main(int argc, char **argv) {
             s.units = u1 - u0;
             tree_locate(g, load(r), u0 - before[r], &s);
             TreeWalk w{};
+            w.begin(g, s, load);
             long long u = u0;
-            int seq = 0;
-            for (w.begin(g, s, load); w.valid(); ++seq) {
-                CHECK(w.seq == seq && w.r < g.requests && w.h < g.kv_heads);
-                CHECK(w.q.n > 0 && w.tokens > 0 && w.tokens <= 2 * g.tpt && w.len > 0);
-                CHECK(w.item_token0(g) + w.tokens <= w.q.n && w.q.t0 + w.q.n <= g.tokens);
-                CHECK(w.tb < w.te && w.te <= w.tiles && w.len <= g.max_rows);
-                const auto key = std::make_tuple(w.r, w.h, w.item);
-                CHECK(done[key] == w.tb);
-                done[key] = w.te;
-                u += w.te - w.tb;
-                if (w.tb == 0) by[key].first = c;
-                by[key].second = c;
-                if (w.te < w.tiles && w.tb == 0)
-                    says[key] = tree_block_of(u + (w.tiles - w.te) - 1, total, blocks);
-                if (w.te < w.tiles) CHECK(u == u1);
-                // the steps of both groups cover the item's tiles
-                int a = 0, b = 0, steps = 0, last = 0;
-                const TreeWalk item = w;
-                bool inside = true;
-                while (inside) {
-                    for (int grp = 0; grp < 2; ++grp) {
-                        if (!w.active(grp)) continue;
-                        CHECK(w.uses(grp));
-                        (grp ? b : a) += 1;
-                        CHECK(w.tile(grp) >= item.tb && w.tile(grp) < item.te);
-                        last += w.last_of(grp);
-                        units += (item.pair ? grp == 0 : true);
-                    }
-                    ++steps;
-                    inside = w.step + 1 < w.steps;
-                    w.next_step(g, load);
+            while (true) {
+                const TreeWalk at = w;
+                const TreeEntry e = w.entry(g, load);
+                if (e.steps == 0) break;
+                const int items = e.kind == kTreeDuo ? 2 : 1;
+                for (int k = 0; k < items; ++k) {
+                    const TreePart &p = e.part[k];
+                    const int per = 2 * g.tpt, item = p.place / per;
+                    const TreeReq q = load(p.r);
+                    const auto key = std::make_tuple(p.r, p.h, item);
+                    const int tiles = tree_item_tiles(g, q, item);
+                    CHECK(p.r < g.requests && p.h < g.kv_heads && item < tree_items(g, q));
+                    CHECK(p.place % per == 0 && p.tok == q.t0 + p.place);
+                    CHECK(p.len == tree_item_len(g, q, item) && p.len > 0 && p.len <= g.max_rows);
+                    CHECK(done[key] == p.first && p.first < p.end && p.end <= tiles);
+                    done[key] = p.end;
+                    u += p.end - p.first;
+                    const bool begins = p.first == 0, whole = begins && p.end == tiles;
+                    CHECK(!!(p.flags & kPartBegins) == begins && !!(p.flags & kPartWhole) == whole);
+                    if (begins) by[key].first = c;
+                    by[key].second = c;
+                    if (begins && !whole) says[key] = tree_block_of(cut, u + (tiles - p.end) - 1);
+                    if (p.end < tiles) CHECK(u == u1);
                 }
-                CHECK(steps == item.steps);
-                CHECK(item.pair ? (a == b && a == item.te - item.tb) : a + b == item.te - item.tb);
-                CHECK(last == 1 + (item.uses(1) ? 1 : 0));
+                // tokens of the row tiles
+                int tokens = 0;
+                for (int k = 0; k < 2; ++k) {
+                    const TreePart &p = e.part[k];
+                    CHECK(p.ntok >= 1 && p.ntok <= g.tpt && p.place + p.ntok <= load(p.r).n);
+                    CHECK(p.tok >= 0 && p.tok + p.ntok <= g.tokens);
+                    if (k == 0 || e.kind == kTreePair) tokens += p.ntok;
+                }
+                if (e.kind != kTreeDuo) CHECK(tokens == at.tokens);
+                CHECK((e.kind == kTreePair) == at.pair(g));
+                // the steps cover each part's tiles, and the parts the entry's
+                std::vector<int> seen[2];
+                for (int st = 0; st < e.steps; ++st)
+                    for (int k = 0; k < 2; ++k)
+                        if (e.part[k].active(st)) {
+                            seen[k].push_back(e.part[k].tile(st));
+                            CHECK(e.part[k].used());
+                            CHECK(e.part[k].last(st) ==
+                                  (e.part[k].tile(st) + e.part[k].stride >= e.part[k].end));
+                        }
+                for (int k = 0; k < 2; ++k) {
+                    CHECK(!e.part[k].active(e.steps));
+                    CHECK(e.part[k].used() == !seen[k].empty());
+                    units += e.kind == kTreePair && k ? 0 : static_cast<int>(seen[k].size());
+                }
+                CHECK(e.part[0].used() && (e.kind == kTreeSplit || e.part[1].used()));
+                if (e.kind == kTreeSplit)
+                    CHECK(static_cast<int>(seen[0].size() + seen[1].size()) == at.te - at.tb);
             }
             CHECK(u == u1);
         }
