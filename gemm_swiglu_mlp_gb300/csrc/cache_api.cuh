@@ -62,10 +62,8 @@ int launch_overlapped(void (*kernel)(Args), dim3 grid, unsigned threads, size_t 
     return SWIGLU_OK;
 }
 
-// Tiles a block takes at least, and the tokens up to which a row tile's
-// queries are fetched token by token (a box of the whole tile reads 128 rows).
+// Tiles a block takes at least.
 constexpr int kTreeMinUnits = 1;
-constexpr int kTreeQOne = 4;
 
 // Workspace of one attention call: which items go on in another block, and
 // two partial results a block (of the item it takes over and of the one it
@@ -100,9 +98,30 @@ bool encode_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map over one cache, [pages * heads][page rows][head size] as 5-D
+// [pages * heads][groups of 8 rows][64-column halves][8 rows][64]: a box is
+// one page of one head and lands as TreeCfg's K and V tiles lie.
+bool encode_pages(CUtensorMap *m, const void *base, int64_t head_dim, int64_t page_size,
+                  uint64_t pages_heads) {
+    EncodeTiledFn enc = get_encode();
+    if (!enc) return false;
+    const cuuint64_t halves = static_cast<cuuint64_t>(head_dim / 64);
+    const cuuint64_t groups = static_cast<cuuint64_t>(page_size / 8);
+    const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+    const cuuint64_t dims[5] = {64, 8, halves, groups, pages_heads};
+    const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(page_size) * row};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(halves),
+                               static_cast<cuuint32_t>(groups), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The attention kernel, one block per SM, and the sums of shared items.
 template <int D>
-int tree_launch(const CUtensorMap &tmQ, const CUtensorMap &tmQ1, const CUtensorMap &tmK,
+int tree_launch(const CUtensorMap &tmQ, const CUtensorMap &tmQn, const CUtensorMap &tmK,
                 const CUtensorMap &tmV, const TreeAttnArgs &a, int sms, void *stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -113,8 +132,8 @@ int tree_launch(const CUtensorMap &tmQ, const CUtensorMap &tmQ1, const CUtensorM
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(sms));
     cfg.blockDim = dim3(kTreeThreads);
-    cfg.dynamicSmemBytes = TreeCfg<D>::SMEM_BYTES;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, tree_attention_kernel<D>, tmQ, tmQ1, tmK, tmV, a);
+    cfg.dynamicSmemBytes = TreeShared<D>::SMEM_BYTES;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, tree_attention_kernel<D>, tmQ, tmQn, tmK, tmV, a);
     if (err == cudaSuccess) {
         cfg.gridDim = dim3(static_cast<unsigned>(2 * sms));
         cfg.blockDim = dim3(kJoinThreads);
@@ -439,21 +458,19 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     a.mask_words = static_cast<int>(mask_words);
     a.part_rows = ws.rows;
     a.min_units = kTreeMinUnits;
-    a.q_one = kTreeQOne;
     const uint64_t pages_heads = static_cast<uint64_t>(num_pages) * static_cast<uint64_t>(kv_heads);
-    CUtensorMap tmQ, tmQ1, tmK, tmV;
+    CUtensorMap tmQ, tmQn, tmK, tmV;
     const uint64_t D = static_cast<uint64_t>(head_dim);
     const uint64_t qh = q_heads > 1 ? q_head_stride : D, qt = tokens > 1 ? q_token_stride : D;
     if (!encode_3d(&tmQ, q, D, q_heads, tokens, qh, qt, static_cast<uint32_t>(group),
                    static_cast<uint32_t>(a.geom.tpt)) ||
-        !encode_3d(&tmQ1, q, D, q_heads, tokens, qh, qt, static_cast<uint32_t>(group), 1) ||
-        !encode_3d(&tmK, k_cache, D, page_size, pages_heads, D, D * page_size,
-                   static_cast<uint32_t>(page_size), 1) ||
-        !encode_3d(&tmV, v_cache, D, page_size, pages_heads, D, D * page_size,
-                   static_cast<uint32_t>(page_size), 1))
+        !encode_3d(&tmQn, q, D, q_heads, tokens, qh, qt, static_cast<uint32_t>(group),
+                   static_cast<uint32_t>(std::max<int64_t>(1, kTreeNarrow / group))) ||
+        !encode_pages(&tmK, k_cache, head_dim, page_size, pages_heads) ||
+        !encode_pages(&tmV, v_cache, head_dim, page_size, pages_heads))
         return SWIGLU_ERR_CUDA;
-    return head_dim == 64 ? tree_launch<64>(tmQ, tmQ1, tmK, tmV, a, st->sm_count, stream)
-                          : tree_launch<128>(tmQ, tmQ1, tmK, tmV, a, st->sm_count, stream);
+    return head_dim == 64 ? tree_launch<64>(tmQ, tmQn, tmK, tmV, a, st->sm_count, stream)
+                          : tree_launch<128>(tmQ, tmQn, tmK, tmV, a, st->sm_count, stream);
 }
 
 }  // extern "C"

@@ -167,10 +167,10 @@ int device_setup(int *dev_out, DeviceState **st_out) {
                                  (2 * kPlanMaxRequests + 1) * 4) != cudaSuccess ||
             cudaFuncSetAttribute(tree_attention_kernel<64>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 TreeCfg<64>::SMEM_BYTES) != cudaSuccess ||
+                                 TreeShared<64>::SMEM_BYTES) != cudaSuccess ||
             cudaFuncSetAttribute(tree_attention_kernel<128>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 TreeCfg<128>::SMEM_BYTES) != cudaSuccess ||
+                                 TreeShared<128>::SMEM_BYTES) != cudaSuccess ||
             // its clusters of up to 16 CTAs (more than the portable 8)
             cudaFuncSetAttribute(down_decode_kernel<32>,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||

@@ -13,28 +13,38 @@
 // (tree_schedule.cuh). All query heads of a kv head and many tokens fill the
 // 128 rows of a row tile, so each K and V tile is read once for up to two row
 // tiles. Roles (12 warps):
-//   warps 0-3, 4-7  softmax groups 0 and 1, one thread per row: scores from
-//                   TMEM, mask, running maximum and sum, weights back to TMEM
-//                   as the A operand of the second product; at an item's end
-//                   the result to memory. The accumulator is only rescaled when
-//                   the maximum has risen by more than 2^8, so most tiles leave
-//                   it alone and weights stay below 2^8.
-//   warp 8          TMA loads: K and V tiles of 128 positions, page by page,
+//   warps 0-3, 4-7  softmax groups 0 and 1 (below)
+//   warp 8          TMA loads: K and V tiles of 128 positions, one box a page,
 //                   through one ring of stages in the order of their use
-//   warp 9          issues the MMAs: S = Q K^T (both K-major), O += P V with P
-//                   from TMEM and V as it lies (MN-major)
+//   warp 9          issues the MMAs
 //   warp 10         tiles with new tokens or past a request's end: zeroes V rows
 //                   past the end and takes NaN and Inf out of new tokens' V
 //                   (0 x NaN would reach rows that do not see them; the rows
 //                   that do get them back at the end)
 //   warp 11         describes the block's entries (tree_schedule.cuh) ahead of
 //                   their use, in a small ring that the other roles read
-// TMEM: scores of the two groups in columns 0-255 (weights alias them), the
-// two accumulators in 256 + D each.
 //
-// While one group's softmax runs, the tensor cores work for the other; how an
-// entry gives both groups work is said at TreeEntry.
-// Every wait is bounded (sm103_ptx.cuh).
+// Two forms, by the rows of a request and kv head (tokens x heads), each with
+// blocks of its own (tree_schedule.cuh):
+//   wide  S = Q K^T with the rows on the 128-row side (TMEM
+//       lanes), one thread a row: no exchange between threads. The weights go
+//       back to TMEM, over the scores, as the A operand of O += P V (V as it
+//       lies, MN-major), in two halves, so that the product begins while the
+//       second half's exponentials are computed.
+//   narrow (up to 32 rows: single tokens, small trees)  S^T = K Q^T with the
+//       positions on the 128-row side, one thread a position: a thread has
+//       as many exponentials as there are rows, where the wide form would
+//       leave 128 to each of a few threads. The weights go to shared memory as
+//       the B operand of O^T += V^T P^T, and of a product with ones that sums
+//       them; the maximum is common to the group: a vote per tile says whether
+//       any score has outgrown it.
+// In both the accumulator is only rescaled when the maximum has risen by more
+// than 2^8, so most tiles leave it alone and weights stay below 2^8.
+// TMEM: scores of the two groups in columns 0-255, the two accumulators in
+// 256 + D each (narrow: sums of p v in 32 columns, sums of p in 32). While one group's softmax runs, the tensor cores work for the
+// other; how an entry gives both groups work is said at TreeEntry.
+// Every wait is bounded (sm103_ptx.cuh); the narrow form's group barriers are
+// reached by all four warps of a group whatever their waits said.
 #pragma once
 
 #include "epilogue.cuh"
@@ -58,36 +68,104 @@ struct TreeAttnArgs {
     int q_heads, num_pages, page_shift, mask_words;
     int part_rows;                     // rows of one partial result: 128 or 256
     int min_units;                     // tiles a block, at least
-    int q_one;                         // up to this many tokens: Q token by token
 };
 
 constexpr int kTreeEntries = 4;   // entries described ahead of their results
+constexpr int kTreeThreads = 384;
+// Registers a thread after the split: the softmax groups hold a row of 128
+// scores; 2 * 128 threads of 200 and 128 of 104 are the 384 * 168 of the launch.
+constexpr int kTreeSoftmaxRegs = 200, kTreeOtherRegs = 104;
 
-template <int D>
+// Shared memory of a block, for either form.
+template <int D, bool NARROW>
 struct TreeCfg {
-    static constexpr int HALVES = D / 64;                  // 64-column halves of a row
-    static constexpr int BLOCK = kTreeTile * kRowBytes;    // one half of a tile: 16 KB
-    static constexpr int TILE = HALVES * BLOCK;            // a Q, K or V tile
-    static constexpr int STAGES = D == 128 ? 5 : 11;
-    static constexpr int OFF_Q = 0;                        // two row tiles
-    static constexpr int OFF_KV = 2 * TILE;
-    static constexpr int OFF_STATS = OFF_KV + STAGES * TILE;   // float2 [2][128]
+    static constexpr int HALVES = D / 64;    // 64-column halves of a row
+    // A K or V tile: 8-row atoms of 1024 bytes, a row group's halves next to
+    // each other, so that a page of both halves is one box and one stretch
+    static constexpr int GROUP = HALVES * 1024;
+    static constexpr int TILE = kTreeTile / 8 * GROUP;
+    // A Q tile: its rows half after half
+    static constexpr int Q_HALF = (NARROW ? kTreeNarrow : kTreeTile) * kRowBytes;
+    static constexpr int QBUF = HALVES * Q_HALF;
+    // Narrow: a group's weights, 128 positions x 32 rows
+    static constexpr int W_BYTES = NARROW ? kTreeTile * kTreeNarrow * 2 : 0;
+    static constexpr int STAGES = D == 128 ? (NARROW ? 6 : 5) : 11;
+    static constexpr int OFF_Q = 0;          // two Q tiles
+    static constexpr int OFF_W = 2 * QBUF;   // two groups' weights
+    static constexpr int OFF_KV = OFF_W + 2 * W_BYTES;
+    static constexpr int END = OFF_KV + STAGES * TILE;
+};
+// What both forms have in common, behind the larger one.
+template <int D>
+struct TreeShared {
+    static constexpr int BASE =
+        TreeCfg<D, true>::END > TreeCfg<D, false>::END ? TreeCfg<D, true>::END : TreeCfg<D, false>::END;
+    static constexpr int OFF_STATS = BASE;                  // float2 [2][128]
     static constexpr int OFF_ENTRY = OFF_STATS + 2 * 128 * 8;
     static constexpr int OFF_BAR = OFF_ENTRY + kTreeEntries * static_cast<int>(sizeof(TreeEntry));
-    // ring: full, empty, V fixed; two Q tiles: full, empty; a group: scores,
-    // weights, result; a warp pair: statistics, results read; entries: full,
-    // empty; drain
-    static constexpr int NUM_BARS = 3 * STAGES + 4 + 6 + 8 + 2 * kTreeEntries + 1;
+    static constexpr int STAGES = 11;                       // the most a form has
+    // ring: full, empty, V fixed; two Q buffers: full, empty; a group: scores,
+    // weights, result, half of the weights; a warp pair: statistics, results
+    // read; entries: full, empty; both groups' statistics (narrow); drain
+    static constexpr int NUM_BARS = 3 * STAGES + 4 + 8 + 8 + 2 * kTreeEntries + 2;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 80;
     static constexpr int TMEM_O = 256;
+    static constexpr int TMEM_ONES = 64;    // narrow: 128 x 16 ones
     static_assert(OFF_BAR % 8 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-constexpr int kTreeThreads = 384;
-// Registers a thread after the split: the softmax groups hold a row of 128
-// scores; 2 * 128 threads of 216 and 128 of 72 are the 384 * 168 of the launch.
-constexpr int kTreeSoftmaxRegs = 216, kTreeOtherRegs = 72;
+// Addresses of the block's mbarriers.
+template <int D>
+struct TreeBars {
+    using S = TreeShared<D>;
+    uint32_t base;
+    __device__ uint32_t at(int i) const { return base + S::OFF_BAR + 8u * i; }
+    __device__ uint32_t kv_full(int s) const { return at(s); }
+    __device__ uint32_t kv_empty(int s) const { return at(S::STAGES + s); }
+    __device__ uint32_t v_fixed(int s) const { return at(2 * S::STAGES + s); }
+    __device__ uint32_t q_full(int b) const { return at(3 * S::STAGES + b); }
+    __device__ uint32_t q_empty(int b) const { return at(3 * S::STAGES + 2 + b); }
+    __device__ uint32_t s_full(int s) const { return at(3 * S::STAGES + 4 + s); }
+    __device__ uint32_t p_ready(int s) const { return at(3 * S::STAGES + 6 + s); }
+    __device__ uint32_t o_full(int s) const { return at(3 * S::STAGES + 8 + s); }
+    __device__ uint32_t p_half(int s) const { return at(3 * S::STAGES + 10 + s); }
+    __device__ uint32_t st_ready(int w) const { return at(3 * S::STAGES + 12 + w); }
+    __device__ uint32_t o_done(int w) const { return at(3 * S::STAGES + 16 + w); }
+    __device__ uint32_t e_full(int i) const { return at(3 * S::STAGES + 20 + i); }
+    __device__ uint32_t e_empty(int i) const { return at(3 * S::STAGES + 20 + kTreeEntries + i); }
+    __device__ uint32_t both_ready() const { return at(3 * S::STAGES + 20 + 2 * kTreeEntries); }
+    __device__ uint32_t drain() const { return at(3 * S::STAGES + 21 + 2 * kTreeEntries); }
+};
+
+// The block's share of one form's line, and where things lie.
+struct TreeBlock {
+    uint8_t *smem;
+    uint32_t tmem;
+    TreeCut cut;
+    int index;       // of the block among its form's
+    int base;        // the form's first block
+};
+
+// Places in shared memory that several roles use.
+template <int D>
+__device__ __forceinline__ float *tree_stats(uint8_t *smem) {
+    return reinterpret_cast<float *>(smem + TreeShared<D>::OFF_STATS);
+}
+template <int D>
+__device__ __forceinline__ TreeEntry *tree_entries(uint8_t *smem) {
+    return reinterpret_cast<TreeEntry *>(smem + TreeShared<D>::OFF_ENTRY);
+}
+template <int D>
+__device__ __forceinline__ volatile int *tree_abort(uint8_t *smem) {
+    return reinterpret_cast<volatile int *>(smem + TreeShared<D>::OFF_MISC + 4);
+}
+// An entry's V had Inf or NaN among its new tokens, [entry][group].
+template <int D>
+__device__ __forceinline__ volatile int *tree_flags(uint8_t *smem) {
+    return reinterpret_cast<volatile int *>(smem + TreeShared<D>::OFF_MISC + 16);
+}
+
 constexpr float kTreeRescale = 8.f;   // rise of the maximum (log2) that rescales
 
 __device__ __forceinline__ float ex2(float x) {
@@ -150,12 +228,12 @@ __device__ __forceinline__ uint32_t tree_visible(const TreeSight &t, int x0) {
 }
 
 // The non-finite V values of the new tokens in positions [x0, x1) that a row
-// sees, added to 32 columns of its result, which this thread has just stored
+// sees, added to `cols` columns of its result, which this thread has just stored
 // (the products took them as zero; nothing finite changes an Inf or a NaN, so
 // adding them to the rounded result is the same). V: the column's place in
 // the kv head's first page, pages `page_step` elements apart.
 template <int D, typename T>
-__device__ __noinline__ void tree_add_nonfinite(T *result, const TreeSight t, int x0, int x1,
+__device__ __noinline__ void tree_add_nonfinite(T *result, int cols, const TreeSight t, int x0, int x1,
                                                 const int *table, int page_shift, int num_pages,
                                                 long long page_step, const uint16_t *v_col) {
     for (int at = x0 & ~31; at < x1; at += 32) {
@@ -167,7 +245,7 @@ __device__ __noinline__ void tree_add_nonfinite(T *result, const TreeSight t, in
             if (page < 0 || page >= num_pages) continue;
             const uint16_t *v =
                 v_col + page * page_step + (x & ((1 << page_shift) - 1)) * static_cast<long long>(D);
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < cols; ++i)
                 if ((v[i] & 0x7F80u) == 0x7F80u) {
                     const float add = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
                     if constexpr (sizeof(T) == 4) {
@@ -187,6 +265,23 @@ __device__ __noinline__ void tree_add_nonfinite(T *result, const TreeSight t, in
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
                                           const volatile int *abort_flag) {
     return __all_sync(~0u, mbar_wait(bar, parity, abort_flag));
+}
+
+// Barriers over the four warps of softmax group s (named barriers 1 and 2).
+__device__ __forceinline__ void group_sync(int s) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
+}
+__device__ __forceinline__ bool group_any(int s, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "bar.red.or.pred q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(1 + s), "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
 }
 
 // Sum over the block of one number a thread: before this thread, and in all.
@@ -211,659 +306,991 @@ __device__ __forceinline__ TreeScan tree_block_scan(long long mine, long long *w
     return s;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kTreeThreads, 1)
-    tree_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
-                          const __grid_constant__ CUtensorMap tmQ1,
-                          const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV,
-                          const __grid_constant__ TreeAttnArgs a) {
-    using C = TreeCfg<D>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t sbase = smem_u32(smem);
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const TreeGeom &g = a.geom;
+// What a role follows: the block's entries, step by step, and the ring's stages
+// in the order that the producer, the MMA issuer and the V warp all keep: per
+// step, for each group in turn, the V tile of this step and the K tile of the
+// next.
+template <int D, bool NARROW>
+struct TreeCursor {
+    using C = TreeCfg<D, NARROW>;
+    const TreeEntry *entries;
+    TreeBars<D> bars;
+    const volatile int *abort_flag;
+    TreeEntry cur, nxt;
+    int step, nstep, seq, stage;
+    uint32_t phase;
 
-    auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * i; };
-    auto kv_full = [&](int s) { return bar(s); };
-    auto kv_empty = [&](int s) { return bar(C::STAGES + s); };
-    auto v_fixed = [&](int s) { return bar(2 * C::STAGES + s); };
-    auto q_full = [&](int b) { return bar(3 * C::STAGES + b); };
-    auto q_empty = [&](int b) { return bar(3 * C::STAGES + 2 + b); };
-    auto s_full = [&](int s) { return bar(3 * C::STAGES + 4 + s); };
-    auto p_ready = [&](int s) { return bar(3 * C::STAGES + 6 + s); };
-    auto o_full = [&](int s) { return bar(3 * C::STAGES + 8 + s); };
-    auto st_ready = [&](int w) { return bar(3 * C::STAGES + 10 + w); };
-    auto o_done = [&](int w) { return bar(3 * C::STAGES + 14 + w); };
-    auto e_full = [&](int i) { return bar(3 * C::STAGES + 18 + i); };
-    auto e_empty = [&](int i) { return bar(3 * C::STAGES + 18 + kTreeEntries + i); };
-    const uint32_t drain_bar = bar(3 * C::STAGES + 18 + 2 * kTreeEntries);
-    float2 *row_stats = reinterpret_cast<float2 *>(smem + C::OFF_STATS);
-    TreeEntry *entries = reinterpret_cast<TreeEntry *>(smem + C::OFF_ENTRY);
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
-    // an entry's V had Inf or NaN among its new tokens, for each group
-    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 16);
-    TreeStart *start = reinterpret_cast<TreeStart *>(smem + C::OFF_MISC + 48);
-    // the prologue's sums, in the statistics' place
-    long long *warp_sums = reinterpret_cast<long long *>(smem + C::OFF_STATS);
-
-    if (warp == 8 && lane == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(kv_full(s), 1);
-            mbar_init(kv_empty(s), 1);
-            mbar_init(v_fixed(s), 1);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(q_full(s), 1);
-            mbar_init(q_empty(s), 1);
-            mbar_init(s_full(s), 1);
-            mbar_init(p_ready(s), 4);
-            mbar_init(o_full(s), 1);
-        }
-        for (int w = 0; w < 4; ++w) {
-            mbar_init(st_ready(w), 2);
-            mbar_init(o_done(w), 2);
-        }
-        for (int i = 0; i < kTreeEntries; ++i) {
-            mbar_init(e_full(i), 1);
-            mbar_init(e_empty(i), 8);
-        }
-        mbar_init(drain_bar, 1);
-        *abort_flag = 0;
-        start->units = 0;
-        fence_barrier_init();
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmQ1);
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-    }
-    if (warp == 9) {
-        tmem_alloc(smem_u32(tmem_holder), 512);
-        tmem_relinquish();
-    }
-    griddep_launch_dependents();
-    griddep_wait();
-
-    // ---- this block's share: sums over the requests, each thread a run of them
-    auto load = [&](int r) {
-        return tree_request(g, a.query_start[r], a.query_start[r + 1], a.ctx_lens[r]);
-    };
-    const int c = static_cast<int>(blockIdx.x);
-    TreeCut cut{};
-    {
-        const int per = (g.requests + kTreeThreads - 1) / kTreeThreads;
-        const int r0 = tree_min(static_cast<int>(threadIdx.x) * per, g.requests);
-        const int r1 = tree_min(r0 + per, g.requests);
-        long long mine = 0;
-        for (int r = r0; r < r1; ++r) mine += g.kv_heads * tree_head_units(g, load(r));
-        const TreeScan scan = tree_block_scan(mine, warp_sums);
-        const int blocks = static_cast<int>(
-            max(1ll, min(static_cast<long long>(gridDim.x), tree_div(scan.total, a.min_units))));
-        cut = tree_cut(scan.total, blocks);
-        const long long u0 = tree_block_begin(cut, c);
-        if (c < blocks && u0 >= scan.before && u0 < scan.before + mine) {
-            long long at = scan.before;
-            for (int r = r0; r < r1; ++r) {
-                const TreeReq q = load(r);
-                const long long u = g.kv_heads * tree_head_units(g, q);
-                if (u0 < at + u) {
-                    start->r = r;
-                    start->units = tree_block_begin(cut, c + 1) - u0;
-                    tree_locate(g, q, u0 - at, start);
-                    break;
-                }
-                at += u;
-            }
+    __device__ __forceinline__ void advance() {
+        if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
         }
     }
-    // rows of no request are zero
-    {
-        const int used = g.requests > 0
-                             ? tree_min(tree_max(a.query_start[g.requests], 0), g.tokens) : 0;
-        const long long per_token = static_cast<long long>(a.q_heads) * D / 8;
-        uint4 *o = reinterpret_cast<uint4 *>(a.out);
-        for (long long i = used * per_token + c * kTreeThreads + threadIdx.x;
-             i < g.tokens * per_token; i += static_cast<long long>(gridDim.x) * kTreeThreads)
-            o[i] = make_uint4(0, 0, 0, 0);
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
-
-    // entry `seq`, once it is described (false: gave up)
-    auto fetch = [&](int seq, TreeEntry &e) {
+    __device__ __forceinline__ bool fetch(TreeEntry &e) {   // entry `seq`, once it is described
         const int i = seq % kTreeEntries;
-        const bool got = mbar_wait(e_full(i), (seq / kTreeEntries) & 1, abort_flag);
+        const bool got = mbar_wait(bars.e_full(i), (seq / kTreeEntries) & 1, abort_flag);
         e = entries[i];
         return got;
-    };
-    // producer bookkeeping for the drain after an abort
+    }
+    __device__ __forceinline__ bool start() {
+        step = seq = stage = 0;
+        phase = 0;
+        return fetch(cur);
+    }
+    __device__ __forceinline__ bool follow() {   // nxt, nstep: the step after (cur, step)
+        nxt = cur;
+        nstep = step + 1;
+        if (nstep < cur.steps) return true;
+        nstep = 0;
+        ++seq;
+        return fetch(nxt);
+    }
+    __device__ __forceinline__ void move() {
+        cur = nxt;
+        step = nstep;
+    }
+    // group s has a tile of its own in a step
+    __device__ __forceinline__ static bool own_kv(const TreeEntry &e, int st, int s) {
+        return e.part[s].active(st) && (s == 0 || e.two_kv());
+    }
+};
+
+// ---- TMA producer: the whole warp walks, lanes issue pages. Returns which
+// stages and Q tiles it filled, and the parity of their last filling, for the
+// drain after an abort.
+template <int D, bool NARROW>
+__device__ __forceinline__ uint2 tree_produce(const CUtensorMap &tmQ, const CUtensorMap &tmK,
+                                              const CUtensorMap &tmV, const TreeAttnArgs &a,
+                                              const TreeBlock &blk) {
+    using C = TreeCfg<D, NARROW>;
+    const TreeGeom &g = a.geom;
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const uint32_t sbase = bars.base;
+    const int lane = threadIdx.x & 31;
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    TreeCursor<D, NARROW> k{tree_entries<D>(blk.smem), bars, abort_flag};
+    bool ok = true;
     uint32_t issued = 0, parity = 0;   // bits: ring stages, then the two Q tiles
+    int qb = 0;
+    uint32_t qphase = 0;
+    const int pages = kTreeTile >> a.page_shift;   // pages a tile, <= 8
+    auto load_tile = [&](const CUtensorMap &tm, const TreePart &x, int tile) {
+        const int left = x.len - tile * kTreeTile;   // positions of the tile, > 0
+        const int count = tree_min(pages, (left + (1 << a.page_shift) - 1) >> a.page_shift);
+        int row = 0;
+        if (lane < count) {
+            const int page = a.table[x.r * a.max_pages +
+                                     static_cast<long long>(tile) * pages + lane];
+            // outside the cache: a box past its end, filled with zeros
+            row = page >= 0 && page < a.num_pages ? page * g.kv_heads + x.h
+                                                  : a.num_pages * g.kv_heads;
+        }
+        if (!warp_wait(bars.kv_empty(k.stage), k.phase ^ 1u, abort_flag)) return false;
+        const uint32_t bytes = static_cast<uint32_t>(count) * kRowBytes * C::HALVES
+                               << a.page_shift;
+        if (lane == 0) mbar_arrive_expect_tx(bars.kv_full(k.stage), bytes);
+        __syncwarp();
+        const uint32_t dst =
+            sbase + C::OFF_KV + k.stage * C::TILE +
+            (static_cast<uint32_t>(lane) * C::HALVES * kRowBytes << a.page_shift);
+        if (lane < count) tma_load_5d(dst, &tm, bars.kv_full(k.stage), 0, 0, 0, 0, row);
+        issued |= 1u << k.stage;
+        parity = (parity & ~(1u << k.stage)) | (k.phase << k.stage);
+        k.advance();
+        return true;
+    };
+    auto load_q = [&](const TreePart &x) {
+        if (!warp_wait(bars.q_empty(qb), ((qphase >> qb) & 1u) ^ 1u, abort_flag)) return false;
+        // a box of the row tile (rows past its tokens are not used)
+        const int toks = (NARROW ? kTreeNarrow : kTreeTile) / g.group;
+        if (lane == 0)
+            mbar_arrive_expect_tx(bars.q_full(qb), static_cast<uint32_t>(toks) * g.group *
+                                                  kRowBytes * C::HALVES);
+        __syncwarp();
+        if (lane < C::HALVES)
+            tma_load_3d(sbase + C::OFF_Q + qb * C::QBUF + lane * C::Q_HALF, &tmQ,
+                        bars.q_full(qb), 64 * lane, x.h * g.group, x.tok);
+        const int bit = C::STAGES + qb;
+        issued |= 1u << bit;
+        parity = (parity & ~(1u << bit)) | (((qphase >> qb) & 1u) << bit);
+        qphase ^= 1u << qb;
+        qb ^= 1;
+        return true;
+    };
+    // group s's K tile of a k.step (Q too at an entry's first)
+    auto load_k = [&](const TreeEntry &e, int st, int s) {
+        if (st == 0 && e.steps > 0 && (s == 0 || e.two_q()) && !load_q(e.part[s]))
+            return false;
+        return !k.own_kv(e, st, s) || load_tile(tmK, e.part[s], e.part[s].tile(st));
+    };
+    ok = __all_sync(~0u, k.start());
+    if (ok && k.cur.steps) ok = load_k(k.cur, 0, 0) && load_k(k.cur, 0, 1);
+    while (ok && k.cur.steps) {
+        ok = __all_sync(~0u, k.follow());
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (!ok) break;
+            if (k.own_kv(k.cur, k.step, s)) ok = load_tile(tmV, k.cur.part[s], k.cur.part[s].tile(k.step));
+            if (k.nxt.steps) ok = ok && load_k(k.nxt, k.nstep, s);
+        }
+        k.move();
+    }
+    if (!ok && lane == 0 && !*abort_flag) {
+        atomicOr(&g_status_word, kStatusProducerTimeout);
+        *abort_flag = 1;
+    }
+    return make_uint2(issued, parity);
+}
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeOtherRegs));
-        // The ring's order, the same for warps 8, 9 and 10: per step, for each
-        // group in turn, the V tile of this step and the K tile of the next.
-        TreeEntry cur{}, nxt{};
-        int step = 0, seq = 0, nstep = 0;
-        bool ok = true;
-        int stage = 0;
-        uint32_t phase = 0;
-        auto advance = [&] {
-            if (++stage == C::STAGES) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        };
-        auto follow = [&] {   // nxt, nstep: the step after (cur, step)
-            nxt = cur;
-            nstep = step + 1;
-            if (nstep < cur.steps) return true;
-            nstep = 0;
-            return fetch(++seq, nxt);
-        };
-        auto own_kv = [](const TreeEntry &e, int st, int s) {   // group s has tiles of its own
-            return e.part[s].active(st) && (s == 0 || e.two_kv());
-        };
-
-        if (warp == 8) {
-            // ---- TMA producer: the whole warp walks, lanes issue pages
-            int qb = 0;
-            uint32_t qphase = 0;
-            const int pages = kTreeTile >> a.page_shift;   // pages a tile, <= 8
-            auto load_tile = [&](const CUtensorMap &tm, const TreePart &x, int tile) {
-                const int left = x.len - tile * kTreeTile;   // positions of the tile, > 0
-                const int count = tree_min(pages, (left + (1 << a.page_shift) - 1) >> a.page_shift);
-                int row = 0;
-                if (lane < count) {
-                    const int page = a.table[x.r * a.max_pages +
-                                             static_cast<long long>(tile) * pages + lane];
-                    // outside the cache: a box past its end, filled with zeros
-                    row = page >= 0 && page < a.num_pages ? page * g.kv_heads + x.h
-                                                          : a.num_pages * g.kv_heads;
-                }
-                if (!warp_wait(kv_empty(stage), phase ^ 1u, abort_flag)) return false;
-                const uint32_t bytes = static_cast<uint32_t>(count) * kRowBytes * C::HALVES
-                                       << a.page_shift;
-                if (lane == 0) mbar_arrive_expect_tx(kv_full(stage), bytes);
-                __syncwarp();
-                const uint32_t dst = sbase + C::OFF_KV + stage * C::TILE +
-                                     (static_cast<uint32_t>(lane) * kRowBytes << a.page_shift);
-                if (lane < count) {
+// ---- MMA issuer: one thread
+template <int D, bool NARROW>
+__device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
+    using C = TreeCfg<D, NARROW>;
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const uint32_t sbase = bars.base;
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    TreeCursor<D, NARROW> k{tree_entries<D>(blk.smem), bars, abort_flag};
+    bool ok = true;
+    // the scores: 128 rows x 128 positions, or 128 positions x 32 rows
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, NARROW ? kTreeNarrow : kTreeTile);
+    // the result: 128 rows x D, V as it lies; or D x 32 rows, both as they lie
+    constexpr uint32_t idesc_o =
+        NARROW ? idesc_bf16_f32(128, kTreeNarrow) | kIdescAMnMajor | kIdescBMnMajor
+               : idesc_bf16_f32(128, D) | kIdescBMnMajor;
+    // narrow: the weights' sums, as a product with a block of ones, so that they
+    // need no registers during the tiles and no exchange between threads
+    constexpr uint32_t idesc_l = idesc_bf16_f32(128, kTreeNarrow) | kIdescBMnMajor;
+    // the first Q buffer of entry k.cur, and of k.nxt
+    int qb = 0, nqb = 0, kstage = 0, vstage = 0;
+    uint32_t qphase = 0, pphase = 0, fphase = 0;
+    auto qbuf = [&](const TreeEntry &e, int b, int s) { return e.two_q() ? b ^ s : b; };
+    // scores of group s for a k.step
+    auto scores = [&](const TreeEntry &e, int st, int s, int b) {
+        const TreePart &x = e.part[s];
+        if (!x.active(st)) return true;
+        const int buf = qbuf(e, b, s);
+        if (st == 0 && (s == 0 || e.two_q())) {
+            if (!mbar_wait(bars.q_full(buf), (qphase >> buf) & 1u, abort_flag)) return false;
+            qphase ^= 1u << buf;
+        }
+        if (s == 0 || e.two_kv()) {
+            if (!mbar_wait(bars.kv_full(k.stage), k.phase, abort_flag)) return false;
+            kstage = k.stage;
+            k.advance();
+        }
+        tc_fence_after();
+        const uint32_t qa = sbase + C::OFF_Q + buf * C::QBUF;
+        const uint64_t kd =
+            smem_desc(sbase + C::OFF_KV + kstage * C::TILE, 16, C::GROUP);
+        const uint64_t qd = smem_desc(qa, 16, 1024);
 #pragma unroll
-                    for (int b = 0; b < C::HALVES; ++b)
-                        tma_load_3d(dst + b * C::BLOCK, &tm, kv_full(stage), 64 * b, 0, row);
-                }
-                issued |= 1u << stage;
-                parity = (parity & ~(1u << stage)) | (phase << stage);
-                advance();
-                return true;
-            };
-            auto load_q = [&](const TreePart &x) {
-                if (!warp_wait(q_empty(qb), ((qphase >> qb) & 1u) ^ 1u, abort_flag)) return false;
-                const bool one = x.ntok <= a.q_one;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(q_full(qb), static_cast<uint32_t>(one ? x.ntok : g.tpt) *
-                                                          g.group * kRowBytes * C::HALVES);
-                __syncwarp();
-                const uint32_t dst = sbase + C::OFF_Q + qb * C::TILE;
-                if (one) {
-                    if (lane < x.ntok)
+        for (int i = 0; i < D / 16; ++i) {
+            const uint64_t ko = kd + (i >> 2) * (1024 >> 4) + 2u * (i & 3);
+            const uint64_t qo = qd + (i >> 2) * (C::Q_HALF >> 4) + 2u * (i & 3);
+            umma_bf16(blk.tmem + 128 * s, NARROW ? ko : qo, NARROW ? qo : ko, idesc_s,
+                      i != 0);
+        }
+        umma_commit(bars.s_full(s));
+        if (s == 1 || e.two_kv()) umma_commit(bars.kv_empty(kstage));
+        // the last scores that need this Q tile
+        if (x.tile(st) + 1 == x.end) umma_commit(bars.q_empty(buf));
+        return true;
+    };
+    ok = k.start();
+    if (ok && k.cur.steps) ok = scores(k.cur, 0, 0, qb) && scores(k.cur, 0, 1, qb);
+    while (ok && k.cur.steps) {
+        ok = k.follow();
+        nqb = k.nstep == 0 && !k.cur.two_q() ? qb ^ 1 : qb;
 #pragma unroll
-                        for (int b = 0; b < C::HALVES; ++b)
-                            tma_load_3d(dst + b * C::BLOCK + lane * g.group * kRowBytes, &tmQ1,
-                                        q_full(qb), 64 * b, x.h * g.group, x.tok + lane);
-                } else if (lane < C::HALVES) {
-                    tma_load_3d(dst + lane * C::BLOCK, &tmQ, q_full(qb), 64 * lane, x.h * g.group,
-                                x.tok);
+        for (int s = 0; s < 2; ++s) {
+            if (!ok) break;
+            const TreePart &x = k.cur.part[s];
+            if (x.active(k.step)) {
+                if (s == 0 || k.cur.two_kv()) {
+                    ok = mbar_wait(bars.kv_full(k.stage), k.phase, abort_flag);
+                    vstage = k.stage;
+                    k.advance();
+                    if (ok && x.edge(x.tile(k.step))) {
+                        ok = mbar_wait(bars.v_fixed(vstage), (fphase >> vstage) & 1u,
+                                       abort_flag);
+                        fphase ^= 1u << vstage;
+                    }
                 }
-                const int bit = C::STAGES + qb;
-                issued |= 1u << bit;
-                parity = (parity & ~(1u << bit)) | (((qphase >> qb) & 1u) << bit);
-                qphase ^= 1u << qb;
-                qb ^= 1;
-                return true;
-            };
-            // group s's K tile of a step (Q too at an entry's first)
-            auto load_k = [&](const TreeEntry &e, int st, int s) {
-                if (st == 0 && e.steps > 0 && (s == 0 || e.two_q()) && !load_q(e.part[s]))
-                    return false;
-                return !own_kv(e, st, s) || load_tile(tmK, e.part[s], e.part[s].tile(st));
-            };
-            ok = __all_sync(~0u, fetch(0, cur));
-            if (ok && cur.steps) ok = load_k(cur, 0, 0) && load_k(cur, 0, 1);
-            while (ok && cur.steps) {
-                ok = __all_sync(~0u, follow());
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
+                const uint64_t vd = smem_desc(sbase + C::OFF_KV + vstage * C::TILE,
+                                              D == 128 ? 1024 : 0, C::GROUP);
+                const uint32_t acc = blk.tmem + TreeShared<D>::TMEM_O + D * s;
+                constexpr uint32_t kstep = 2 * C::GROUP >> 4;   // 16 positions of V
+                if constexpr (NARROW) {
+                    ok = ok && mbar_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
                     if (!ok) break;
-                    if (own_kv(cur, step, s)) ok = load_tile(tmV, cur.part[s], cur.part[s].tile(step));
-                    if (nxt.steps) ok = ok && load_k(nxt, nstep, s);
-                }
-                cur = nxt;
-                step = nstep;
-            }
-            if (!ok && lane == 0 && !*abort_flag) {
-                atomicOr(&g_status_word, kStatusProducerTimeout);
-                *abort_flag = 1;
-            }
-        } else if (warp == 9) {
-            // ---- MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kTreeTile);
-                constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
-                int qb = 0, kstage = 0, vstage = 0;
-                uint32_t qphase = 0, pphase = 0, fphase = 0;
-                // scores of group s for a step
-                auto scores = [&](const TreeEntry &e, int st, int s) {
-                    const TreePart &x = e.part[s];
-                    if (!x.active(st)) return true;
-                    const int buf = qb ^ (e.two_q() ? s : 0);
-                    if (st == 0 && (s == 0 || e.two_q())) {
-                        if (!mbar_wait(q_full(buf), (qphase >> buf) & 1u, abort_flag)) return false;
-                        qphase ^= 1u << buf;
-                    }
-                    if (s == 0 || e.two_kv()) {
-                        if (!mbar_wait(kv_full(stage), phase, abort_flag)) return false;
-                        kstage = stage;
-                        advance();
-                    }
                     tc_fence_after();
-                    const uint64_t qd = smem_desc_k128(sbase + C::OFF_Q + buf * C::TILE);
-                    const uint64_t kd = smem_desc_k128(sbase + C::OFF_KV + kstage * C::TILE);
+                    const uint64_t wd =
+                        smem_desc(sbase + C::OFF_W + s * C::W_BYTES, 16, 512, 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * (C::BLOCK >> 4) + 2u * (k & 3);
-                        umma_bf16(tmem + 128 * s, qd + off, kd + off, idesc_qk, k != 0);
-                    }
-                    umma_commit(s_full(s));
-                    if (s == 1 || e.two_kv()) umma_commit(kv_empty(kstage));
-                    // the last scores that need this Q tile
-                    if (x.tile(st) + 1 == x.end) {
-                        umma_commit(q_empty(buf));
-                        if (!e.two_q()) qb ^= 1;
-                    }
-                    return true;
-                };
-                ok = fetch(0, cur);
-                if (ok && cur.steps) ok = scores(cur, 0, 0) && scores(cur, 0, 1);
-                while (ok && cur.steps) {
-                    ok = follow();
+                    for (int i = 0; i < kTreeTile / 16; ++i)
+                        umma_bf16(acc, vd + kstep * i, wd + 64u * i, idesc_o,
+                                  k.step != 0 || i != 0);
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (!ok) break;
-                        const TreePart &x = cur.part[s];
-                        if (x.active(step)) {
-                            if (s == 0 || cur.two_kv()) {
-                                ok = mbar_wait(kv_full(stage), phase, abort_flag);
-                                vstage = stage;
-                                advance();
-                                if (ok && x.edge(x.tile(step))) {
-                                    ok = mbar_wait(v_fixed(vstage), (fphase >> vstage) & 1u,
-                                                   abort_flag);
-                                    fphase ^= 1u << vstage;
-                                }
-                            }
-                            ok = ok && mbar_wait(p_ready(s), (pphase >> s) & 1u, abort_flag);
-                            if (!ok) break;
-                            pphase ^= 1u << s;
-                            tc_fence_after();
-                            const uint64_t vd =
-                                smem_desc_mn128(sbase + C::OFF_KV + vstage * C::TILE, C::BLOCK);
-#pragma unroll
-                            for (int k = 0; k < kTreeTile / 16; ++k)
-                                umma_bf16_ts(tmem + C::TMEM_O + D * s, tmem + 128 * s + 8 * k,
-                                             vd + 128u * k, idesc_pv, step != 0 || k != 0);
-                            if (s == 1 || cur.two_kv()) umma_commit(kv_empty(vstage));
-                            if (x.last(step)) umma_commit(o_full(s));
-                        }
-                        if (nxt.steps) ok = scores(nxt, nstep, s);
-                    }
-                    cur = nxt;
-                    step = nstep;
-                }
-                if (!ok && !*abort_flag) {
-                    atomicOr(&g_status_word, kStatusMmaTimeout);
-                    *abort_flag = 1;
-                }
-            }
-        } else if (warp == 10) {
-            // ---- V rows of edge tiles. Every stage is waited for in ring
-            // order, K's and those of tiles that need nothing too: a wait on a
-            // stage a whole pass ahead would take the pass before for it.
-            auto pass = [&] {
-                const bool full = warp_wait(kv_full(stage), phase, abort_flag);
-                advance();
-                return full;
-            };
-            ok = __all_sync(~0u, fetch(0, cur));
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (ok && cur.steps && own_kv(cur, 0, s)) ok = pass();
-            while (ok && cur.steps) {
-                const int slot = seq % kTreeEntries;
-                ok = __all_sync(~0u, follow());
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
+                    for (int i = 0; i < kTreeTile / 16; ++i)
+                        umma_bf16_ts(acc + 32, blk.tmem + TreeShared<D>::TMEM_ONES, wd + 64u * i,
+                                     idesc_l, k.step != 0 || i != 0);
+                } else {
+                    ok = ok && mbar_wait(bars.p_half(s), (pphase >> s) & 1u, abort_flag);
                     if (!ok) break;
-                    if (own_kv(cur, step, s)) {
-                        const int at = stage;
-                        ok = pass();
-                        if (!ok) break;
-                        const TreePart &x = cur.part[s];
-                        if (x.edge(x.tile(step))) {
-                            const int x0 = x.tile(step) * kTreeTile;
-                            // rows [first, end) hold new tokens, [end, 128) nothing;
-                            // a row's 16-byte chunks are permuted within its 128 bytes
-                            const int end = tree_min(x.len - x0, kTreeTile);
-                            const int first = tree_min(tree_max(x.ctx - x0, 0), end);
-                            bool bad = false;
-                            for (int b = 0; b < C::HALVES; ++b) {
-                                uint4 *base = reinterpret_cast<uint4 *>(
-                                    smem + C::OFF_KV + at * C::TILE + b * C::BLOCK);
-                                for (int i = end * 8 + lane; i < kTreeTile * 8; i += 32)
-                                    base[i] = make_uint4(0, 0, 0, 0);
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < kTreeTile / 32; ++i)
+                        umma_bf16_ts(acc, blk.tmem + 128 * s + 8 * i, vd + kstep * i,
+                                     idesc_o, k.step != 0 || i != 0);
+                    ok = mbar_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = kTreeTile / 32; i < kTreeTile / 16; ++i)
+                        umma_bf16_ts(acc, blk.tmem + 128 * s + 8 * i, vd + kstep * i,
+                                     idesc_o, 1u);
+                }
+                pphase ^= 1u << s;
+                if (s == 1 || k.cur.two_kv()) umma_commit(bars.kv_empty(vstage));
+                if (x.last(k.step)) umma_commit(bars.o_full(s));
+            }
+            if (k.nxt.steps) ok = scores(k.nxt, k.nstep, s, nqb);
+        }
+        k.move();
+        qb = nqb;
+    }
+    if (!ok && !*abort_flag) {
+        atomicOr(&g_status_word, kStatusMmaTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// ---- V rows of edge tiles. Every stage is waited for and given back in ring
+// order, K's and those of tiles that need nothing too, so that this warp is
+// never a whole pass of the ring away from the others (a wait on a barrier's
+// parity cannot tell two passes apart).
+template <int D, bool NARROW>
+__device__ __forceinline__ void tree_mend_v(const TreeBlock &blk) {
+    using C = TreeCfg<D, NARROW>;
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const int lane = threadIdx.x & 31;
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    volatile int *flags = tree_flags<D>(blk.smem);
+    TreeCursor<D, NARROW> k{tree_entries<D>(blk.smem), bars, abort_flag};
+    bool ok = true;
+    auto pass = [&] {
+        const bool full = warp_wait(bars.kv_full(k.stage), k.phase, abort_flag);
+        if (lane == 0) mbar_arrive(bars.kv_empty(k.stage));
+        k.advance();
+        return full;
+    };
+    ok = __all_sync(~0u, k.start());
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+        if (ok && k.cur.steps && k.own_kv(k.cur, 0, s)) ok = pass();
+    while (ok && k.cur.steps) {
+        const int slot = k.seq % kTreeEntries;
+        ok = __all_sync(~0u, k.follow());
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (!ok) break;
+            if (k.own_kv(k.cur, k.step, s)) {
+                const int at = k.stage;
+                ok = warp_wait(bars.kv_full(at), k.phase, abort_flag);
+                if (!ok) break;
+                const TreePart &x = k.cur.part[s];
+                if (x.edge(x.tile(k.step))) {
+                    const int x0 = x.tile(k.step) * kTreeTile;
+                    // rows [first, end) hold new tokens, [end, 128) nothing;
+                    // a row's 16-byte chunks are permuted within its 128 bytes
+                    const int end = tree_min(x.len - x0, kTreeTile);
+                    const int first = tree_min(tree_max(x.ctx - x0, 0), end);
+                    bool bad = false;
+                    // 16-byte chunk i of the rows' halves, row by row
+                    uint8_t *base = blk.smem + C::OFF_KV + at * C::TILE;
+                    constexpr int chunks = C::HALVES * 8;   // a row
+                    auto chunk = [&](int i) {
+                        const int r = i / chunks, k = i % chunks;
+                        return reinterpret_cast<uint4 *>(
+                            base + (r >> 3) * C::GROUP + (k >> 3) * 1024 +
+                            (r & 7) * kRowBytes + (k & 7) * 16);
+                    };
+                    for (int i = end * chunks + lane; i < kTreeTile * chunks; i += 32)
+                        *chunk(i) = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
-                                for (int i = first * 8 + lane; i < end * 8; i += 32) {
-                                    uint4 v = base[i];
-                                    uint32_t any = 0;   // exponent all ones: carry
-                                    any |= (v.x & 0x7F807F80u) + 0x00800080u;
-                                    any |= (v.y & 0x7F807F80u) + 0x00800080u;
-                                    any |= (v.z & 0x7F807F80u) + 0x00800080u;
-                                    any |= (v.w & 0x7F807F80u) + 0x00800080u;
-                                    if (any & 0x80008000u) {
-                                        uint32_t *e = reinterpret_cast<uint32_t *>(base + i);
-                                        for (int k = 0; k < 4; ++k) {
-                                            uint32_t z = e[k];
-                                            if ((z & 0x7F80u) == 0x7F80u) z &= 0xFFFF0000u;
-                                            if ((z & 0x7F800000u) == 0x7F800000u) z &= 0xFFFFu;
-                                            e[k] = z;
-                                        }
-                                        bad = true;
-                                    }
-                                }
+                    for (int i = first * chunks + lane; i < end * chunks; i += 32) {
+                        uint4 *at16 = chunk(i);
+                        const uint4 v = *at16;
+                        uint32_t any = 0;   // exponent all ones: carry
+                        any |= (v.x & 0x7F807F80u) + 0x00800080u;
+                        any |= (v.y & 0x7F807F80u) + 0x00800080u;
+                        any |= (v.z & 0x7F807F80u) + 0x00800080u;
+                        any |= (v.w & 0x7F807F80u) + 0x00800080u;
+                        if (any & 0x80008000u) {
+                            uint32_t *e = reinterpret_cast<uint32_t *>(at16);
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t z = e[k];
+                                if ((z & 0x7F80u) == 0x7F80u) z &= 0xFFFF0000u;
+                                if ((z & 0x7F800000u) == 0x7F800000u) z &= 0xFFFFu;
+                                e[k] = z;
                             }
-                            if (bad) {
-                                flags[2 * slot + s] = 1;
-                                if (!cur.two_kv()) flags[2 * slot + 1] = 1;
-                            }
-                            __threadfence_block();
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(v_fixed(at));
+                            bad = true;
                         }
                     }
-                    if (nxt.steps && own_kv(nxt, nstep, s)) ok = ok && pass();
+                    if (bad) {
+                        flags[2 * slot + s] = 1;
+                        if (!k.cur.two_kv()) flags[2 * slot + 1] = 1;
+                    }
+                    __threadfence_block();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.v_fixed(at));
                 }
-                cur = nxt;
-                step = nstep;
+                if (lane == 0) mbar_arrive(bars.kv_empty(at));
+                k.advance();
             }
-            if (!ok && lane == 0 && !*abort_flag) {
-                atomicOr(&g_status_word, kStatusEpilogueTimeout);
-                *abort_flag = 1;
-            }
-        } else if (lane == 0) {
-            // ---- entries, ahead of their use
-            TreeWalk w{};
-            w.begin(g, *start, load);
-            int4 chain = make_int4(0, 0, 0, 0);
-            for (bool more = true; more && ok; ++seq) {
-                const int i = seq % kTreeEntries;
-                const TreeEntry e = w.entry(g, load);
-                more = e.steps > 0;
-                ok = mbar_wait(e_empty(i), ((seq / kTreeEntries) & 1) ^ 1, abort_flag);
-                if (!ok) break;
-                entries[i] = e;
-                flags[2 * i] = flags[2 * i + 1] = 0;
-                mbar_arrive(e_full(i));
-                // an item that begins here and goes on in the next blocks
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (!more) break;
-                    const TreePart &x = e.part[s];
-                    if ((x.flags & (kPartWhole | kPartBegins | kPartSecond)) != kPartBegins) continue;
-                    const int rest = (x.len + kTreeTile - 1) / kTreeTile - x.end;
-                    chain = make_int4(tree_block_of(cut, tree_block_begin(cut, c + 1) + rest - 1),
-                                      x.tok, x.h,
-                                      x.ntok + (e.kind == kTreePair ? e.part[1].ntok : 0));
-                }
-            }
-            a.chains[c] = chain;
-            if (!ok && !*abort_flag) {
-                atomicOr(&g_status_word, kStatusProducerTimeout);
-                *abort_flag = 1;
-            }
+            if (k.nxt.steps && k.own_kv(k.nxt, k.nstep, s)) ok = ok && pass();
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftmaxRegs));
-        // ---- softmax group s, one thread a row
-        const int s = warp >> 2, quad = warp & 3;
-        const int row = 32 * quad + lane;
-        const int my_tok = row / g.group, my_head = row - my_tok * g.group;
-        const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-        const uint32_t ts = tmem + lanes + 128 * s;                  // scores, weights
-        const uint32_t to = tmem + lanes + C::TMEM_O + D * s;        // own accumulator
-        uint32_t sphase = 0, ophase0 = 0, ophase1 = 0, xphase = 0;
-        bool ok = true, merged = false;   // merged: results were shared, o_done is due
-        for (int seq = 0;; ++seq) {
-            const int slot = seq % kTreeEntries;
-            ok = warp_wait(e_full(slot), (seq / kTreeEntries) & 1, abort_flag);
-            if (!ok) break;
-            const TreeEntry &entry = entries[slot];
-            if (entry.steps == 0) break;
-            // most of it stays in shared memory: the scores need the registers
-            const TreePart &x = entry.part[s];
-            const bool warp_on = 32 * quad < x.ntok * g.group;
-            const bool row_on = my_tok < x.ntok;
-            auto sight = [&] {
-                return TreeSight{a.mask ? a.mask + static_cast<long long>(x.tok + my_tok) *
-                                                       a.mask_words
-                                        : nullptr,
-                                 a.mask_words, x.place + my_tok, x.ctx, x.len};
-            };
-            float m = -INFINITY, l = 0.f;
-            bool fresh = true;
-            for (int tile = x.first; tile < x.end; tile += x.stride) {
-                ok = warp_wait(s_full(s), sphase, abort_flag);
-                if (!ok) break;
-                sphase ^= 1u;
-                if (warp_on) {
-                    tc_fence_after();
-                    uint32_t v[4][32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, v[i]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) reg_fence32(v[i]);
-                    if (x.edge(tile)) {
-                        const TreeSight t = sight();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t see =
-                                row_on ? tree_visible(t, tile * kTreeTile + 32 * i) : 0u;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!((see >> j) & 1u)) v[i][j] = 0xFF800000u;
-                        }
-                    }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-                            mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3],
-                                                     fmaxf(__uint_as_float(v[i][j]),
-                                                           __uint_as_float(v[i][j + 1])));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (fresh) {
-                        m = top;
-                        fresh = false;
-                    } else {
-                        const bool rise = top * a.scale_log2 > m * a.scale_log2 + kTreeRescale;
-                        if (__any_sync(~0u, rise && row_on)) {
-                            const float f = rise ? ex2((m - top) * a.scale_log2) : 1.f;
-                            m = rise ? top : m;
-                            l *= f;
-#pragma unroll 1
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t o[32];
-                                tmem_ld_32x32b_x32(to + 32 * i, o);
-                                tmem_ld_wait();
-                                reg_fence32(o);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st_32x32b_x32(to + 32 * i, o);
-                            }
-                        }
-                    }
-                    // an all-masked row so far: weights 2^(-inf - 0) = 0
-                    const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float lo, hi;
-                            fma2(lo, hi, __uint_as_float(v[i][2 * j]),
-                                 __uint_as_float(v[i][2 * j + 1]), a.scale_log2, base);
-                            lo = ex2(lo);
-                            hi = ex2(hi);
-                            add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
-                            p[j] = pack_bf16x2(lo, hi);
-                        }
-                        tmem_st_32x32b_x16(ts + 16 * i, p);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                }
-                // the accumulator of the entry before has been read by both groups
-                if (merged) {
-                    ok = warp_wait(o_done(quad), xphase ^ 1u, abort_flag);
-                    if (!ok) break;
-                    merged = false;
-                }
-                if (warp_on) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready(s));
-            }
-            if (!ok) break;
+        if (k.nstep == 0 && lane == 0) mbar_arrive(bars.e_empty(slot));
+        k.move();
+    }
+    if (!ok && lane == 0 && !*abort_flag) {
+        atomicOr(&g_status_word, kStatusEpilogueTimeout);
+        *abort_flag = 1;
+    }
+}
 
-            // ---- the entry's end: this block's result
-            const bool whole = (x.flags & kPartWhole) != 0;
-            // partial results: slot 2c + 1 for an item that begins here, 2c for others
-            const long long prow =
-                static_cast<long long>(2 * c + ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows +
-                ((x.flags & kPartSecond) ? 128 : 0) + row;
-            const bool split = entry.kind == kTreeSplit;
-            const bool used1 = entry.part[1].used();
-            int first = x.first;              // this block's tiles of the item
-            float w0 = 1.f, w1 = 0.f;
-            int c0 = 0, c1 = D;               // columns that this thread writes
-            if (split) {
-                // merge the groups' statistics; each writes half of the columns
-                first = entry.part[0].first;
-                if (x.used()) row_stats[128 * s + row] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(st_ready(quad));
-                ok = warp_wait(st_ready(quad), xphase, abort_flag);
-                if (!ok) break;
-                const float2 a0 = row_stats[row];
-                const float2 a1 = used1 ? row_stats[128 + row] : make_float2(-INFINITY, 0.f);
-                m = fmaxf(a0.x, a1.x);
-                w0 = a0.x == -INFINITY ? 0.f : ex2((a0.x - m) * a.scale_log2);
-                w1 = a1.x == -INFINITY ? 0.f : ex2((a1.x - m) * a.scale_log2);
-                l = a0.y * w0 + a1.y * w1;
-                c0 = s * (D / 2);
-                c1 = c0 + D / 2;
-            }
-            if (split || s == 0) ok = warp_wait(o_full(0), ophase0, abort_flag);
-            if (ok && used1 && (split || s == 1)) ok = warp_wait(o_full(1), ophase1, abort_flag);
-            if (!ok) break;
-            ophase0 ^= 1u;
-            if (used1) ophase1 ^= 1u;
-            tc_fence_after();
-            const bool flagged = flags[2 * slot + s] || (split && flags[2 * slot + (s ^ 1)]);
-            if (warp_on) {
-                if (!whole && row_on && (!split || s == 0)) a.stats[prow] = make_float2(m, l);
-                const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const uint32_t t0 = tmem + lanes + C::TMEM_O, t1 = t0 + D;
-#pragma unroll 1
-                for (int col = c0; col < c1; col += 32) {
-                    uint32_t o[32];
-                    if (!split) {
-                        tmem_ld_32x32b_x32(to + col, o);
-                        tmem_ld_wait();
-                        reg_fence32(o);
-                    } else {
-                        tmem_ld_32x32b_x32(t0 + col, o);
-                        uint32_t y[32];
-                        if (used1) tmem_ld_32x32b_x32(t1 + col, y);
-                        tmem_ld_wait();
-                        reg_fence32(o);
-                        if (used1) {
-                            reg_fence32(y);
+// ---- entries, ahead of their use: one thread
+template <int D, typename Load>
+__device__ __forceinline__ void tree_describe(const TreeAttnArgs &a, const TreeBlock &blk,
+                                              const TreeStart &start, Load load) {
+    const TreeGeom &g = a.geom;
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    volatile int *flags = tree_flags<D>(blk.smem);
+    TreeEntry *entries = tree_entries<D>(blk.smem);
+    TreeWalk w{};
+    w.begin(g, start, load);
+    int4 chain = make_int4(0, 0, 0, 0);
+    bool ok = true;
+    int seq = 0;
+    for (bool more = true; more; ++seq) {
+        const int i = seq % kTreeEntries;
+        const TreeEntry e = w.entry(g, load);
+        more = e.steps > 0;
+        ok = mbar_wait(bars.e_empty(i), ((seq / kTreeEntries) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        entries[i] = e;
+        flags[2 * i] = flags[2 * i + 1] = 0;
+        mbar_arrive(bars.e_full(i));
+        // an item that begins here and goes on in the next blocks
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                o[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), w1,
-                                                            __uint_as_float(o[j]) * w0));
-                        }
-                    }
-                    if (!row_on) continue;
-                    uint16_t *const out = a.out + (static_cast<long long>(x.tok + my_tok) * a.q_heads +
-                                                   x.h * g.group + my_head) * D + col;
-                    float *const sums = a.partial + prow * D + col;
-                    if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(out);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t b[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                b[k] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * k]) * inv,
-                                                   __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
-                            dst[j] = make_uint4(b[0], b[1], b[2], b[3]);
-                        }
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(sums);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    }
-                    if (flagged) {
-                        const int x0 = tree_max(x.ctx, first * kTreeTile);
-                        const int x1 = tree_min(x.len, x.end * kTreeTile);
-                        const long long head_step = static_cast<long long>(D) << a.page_shift;
-                        const uint16_t *vc = a.v_cache + x.h * head_step + col;
-                        const int *table = a.table + x.r * a.max_pages;
-                        if (whole)
-                            tree_add_nonfinite<D>(out, sight(), x0, x1, table, a.page_shift,
-                                                  a.num_pages, g.kv_heads * head_step, vc);
-                        else
-                            tree_add_nonfinite<D>(sums, sight(), x0, x1, table, a.page_shift,
-                                                  a.num_pages, g.kv_heads * head_step, vc);
-                    }
-                }
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (split) {
-                if (lane == 0) mbar_arrive(o_done(quad));
-                merged = true;
-                xphase ^= 1u;
-            }
-            if (lane == 0) mbar_arrive(e_empty(slot));
+        for (int s = 0; s < 2; ++s) {
+            const TreePart &x = e.part[s];
+            if (!more || (x.flags & (kPartWhole | kPartBegins | kPartSecond)) != kPartBegins) continue;
+            const int rest = (x.len + kTreeTile - 1) / kTreeTile - x.end;
+            const long long last = tree_block_begin(blk.cut, blk.index + 1) + rest - 1;
+            chain = make_int4(blk.base + tree_block_of(blk.cut, last), x.tok, x.h,
+                              x.ntok + (e.kind == kTreePair ? e.part[1].ntok : 0));
         }
+    }
+    a.chains[blockIdx.x] = chain;
+    if (!ok && !*abort_flag) {
+        atomicOr(&g_status_word, kStatusProducerTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// Where a softmax warp is in the barriers' phases.
+struct TreePhase {
+    uint32_t scores, own[2], merge, both;   // s_full, o_full of each group, o_done, both_ready
+    bool merged;                            // the entry before was shared: o_done is due
+};
+
+// The entry before, if the groups shared it: all eight warps have read its
+// statistics and accumulators.
+template <int D>
+__device__ __forceinline__ bool tree_results_read(const TreeBars<D> &bars, TreePhase &ph,
+                                                  const volatile int *abort_flag) {
+    bool read = true;
+    if (ph.merged)
+        for (int q = 0; q < 4; ++q)
+            read = read && warp_wait(bars.o_done(q), ph.merge ^ 1u, abort_flag);
+    ph.merged = false;
+    return read;
+}
+
+// The largest of a warp's values (NaN left out).
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// ---- softmax, narrow form. One entry's part, for the warps of one group: a
+// thread is position `row` of each tile, and column d = row of the result.
+// False: gave up (the abort flag is set before any group barrier that follows).
+// Rows go by eights in loops that are not unrolled: with them unrolled the
+// code does not fit the instruction cache beside the other roles' (first
+// tiles and results then took 6000 cycles each).
+template <int D>
+__device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const TreeBlock &blk,
+                                                 const TreeEntry &entry, int slot, TreePhase &ph) {
+    using C = TreeCfg<D, true>;
+    const TreeGeom &g = a.geom;
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = warp >> 2, quad = warp & 3;
+    const int row = 32 * quad + lane;
+    const int c = static_cast<int>(blockIdx.x);
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t ts = blk.tmem + lanes + 128 * s;                            // scores
+    const uint32_t to = blk.tmem + lanes + TreeShared<D>::TMEM_O + D * s;      // sums of p v
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    volatile int *flags = tree_flags<D>(blk.smem);
+    // a group's statistics: its warps' maxima [4][32], the maximum [32], its
+    // last rescale factor [32], and what is added to scale * score [32]:
+    // -scale * maximum, or a number that makes any score rise while there is
+    // no maximum
+    constexpr int kMax = 128, kFactor = 160, kAdd = 192;
+    constexpr float kNoMax = 1e30f;
+    float *group_stats = tree_stats<D>(blk.smem) + 256 * s;
+    const TreePart &x = entry.part[s];
+    const int rows = x.ntok * g.group;
+    const bool split = entry.kind == kTreeSplit;
+    const bool used1 = entry.part[1].used();
+    const float sc = a.scale_log2;
+    bool good = true;
+    auto give_up = [&] {
+        if (lane == 0 && !*abort_flag) {
+            atomicOr(&g_status_word, kStatusEpilogueTimeout);
+            *abort_flag = 1;
+        }
+        good = false;
+    };
+    if (!tree_results_read<D>(bars, ph, abort_flag)) give_up();
+    if (quad == 0) {
+        group_stats[kMax + lane] = -INFINITY;
+        group_stats[kAdd + lane] = kNoMax;
+    }
+    uint8_t *const weights = blk.smem + C::OFF_W + s * C::W_BYTES + row * (2 * kTreeNarrow);
+    const int swizzle = 16 * ((row >> 1) & 3);   // 64-byte rows, 64-byte swizzle
+    for (int tile = x.first; tile < x.end; tile += x.stride) {
+        if (good && !warp_wait(bars.s_full(s), ph.scores, abort_flag)) give_up();
+        ph.scores ^= 1u;
+        tc_fence_after();
+        // bit n: row n sees this position
+        uint32_t see = ~0u;
+        if (x.edge(tile)) {
+            const int pos = tile * kTreeTile + row;
+            see = pos < tree_min(x.ctx, x.len) ? ~0u : 0u;
+            if (pos >= x.ctx && pos < x.len) {
+                const int j = pos - x.ctx;
+                const uint32_t heads = mask_of_bits(g.group);
+                for (int t = 0; t < x.ntok; ++t) {
+                    const bool on =
+                        a.mask ? (j >> 6) < a.mask_words &&
+                                     ((a.mask[static_cast<long long>(x.tok + t) * a.mask_words +
+                                              (j >> 6)] >> (j & 63)) & 1)
+                               : j <= x.place + t;
+                    if (on) see |= heads << (t * g.group);
+                }
+            }
+        }
+        auto scores = [&](int n0, uint32_t (&v)[8]) {
+            tmem_ld_32x32b_x8(ts + n0, v);
+            tmem_ld_wait();
+            reg_fence8(v);
+            if (see != ~0u) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    if (!((see >> (n0 + n)) & 1u)) v[n] = 0xFF800000u;
+            }
+        };
+        bool first = tile == x.first;
+        for (bool again = true;; again = false) {
+            // weights by the maximum so far, as if no score had outgrown it
+            bool rise = false;
+#pragma unroll 1
+            for (int n0 = 0; n0 < rows && good; n0 += 8) {
+                uint32_t v[8];
+                scores(n0, v);
+                float add[8];
+                *reinterpret_cast<float4 *>(add) =
+                    *reinterpret_cast<const float4 *>(group_stats + kAdd + n0);
+                *reinterpret_cast<float4 *>(add + 4) =
+                    *reinterpret_cast<const float4 *>(group_stats + kAdd + n0 + 4);
+                float e[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    e[n] = fmaf(__uint_as_float(v[n]), sc, first ? kNoMax : add[n]);
+                    rise = rise || (n0 + n < rows && e[n] > kTreeRescale);
+                }
+                uint32_t p[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) p[n] = pack_bf16x2(ex2(e[2 * n]), ex2(e[2 * n + 1]));
+                *reinterpret_cast<uint4 *>(weights + ((2 * n0) ^ swizzle)) =
+                    make_uint4(p[0], p[1], p[2], p[3]);
+            }
+            // (once a tile: scores of 1e9 and more can be past it by rounding)
+            const bool risen = group_any(s, rise && good && again);
+            if (*abort_flag) good = false;
+            if (!risen) break;
+            // new maxima: each warp's, then the group's
+#pragma unroll 1
+            for (int n0 = 0; n0 < rows && good; n0 += 8) {
+                uint32_t v[8];
+                scores(n0, v);
+                float top[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) top[n] = warp_max(__uint_as_float(v[n]));
+                if (lane == 0) {
+                    float4 *at = reinterpret_cast<float4 *>(group_stats + 32 * quad + n0);
+                    at[0] = make_float4(top[0], top[1], top[2], top[3]);
+                    at[1] = make_float4(top[4], top[5], top[6], top[7]);
+                }
+            }
+            group_sync(s);
+            if (quad == 0 && lane < rows) {
+                const float old = group_stats[kMax + lane];
+                const float top = fmaxf(fmaxf(fmaxf(group_stats[lane], group_stats[32 + lane]),
+                                              fmaxf(group_stats[64 + lane], group_stats[96 + lane])),
+                                        old);
+                group_stats[kMax + lane] = top;
+                group_stats[kFactor + lane] = top > old ? ex2((old - top) * sc) : 1.f;
+                group_stats[kAdd + lane] = top == -INFINITY ? kNoMax : -top * sc;
+            }
+            group_sync(s);
+            if (!first && tile != x.first) {
+                // the sums of p v (columns 0 - 31) and of p (32 - 63)
+#pragma unroll 1
+                for (int n0 = 0; n0 < rows && good; n0 += 8) {
+                    uint32_t o[8], l[8];
+                    tmem_ld_32x32b_x8(to + n0, o);
+                    tmem_ld_32x32b_x8(to + 32 + n0, l);
+                    tmem_ld_wait();
+                    reg_fence8(o);
+                    reg_fence8(l);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const float f = group_stats[kFactor + n0 + n];
+                        o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+                        l[n] = __float_as_uint(__uint_as_float(l[n]) * f);
+                    }
+                    tmem_st_32x32b_x8(to + n0, o);
+                    tmem_st_32x32b_x8(to + 32 + n0, l);
+                }
+                tmem_st_wait();
+            }
+            first = false;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (good && lane == 0) mbar_arrive(bars.p_ready(s));
+    }
+
+    // ---- this block's result
+    if (split) {   // the other group's maxima
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.both_ready());
+        if (good && !warp_wait(bars.both_ready(), ph.both, abort_flag)) give_up();
+        ph.both ^= 1u;
+    }
+    if (good && (split || s == 0) && !warp_wait(bars.o_full(0), ph.own[0], abort_flag)) give_up();
+    if (good && used1 && (split || s == 1) && !warp_wait(bars.o_full(1), ph.own[1], abort_flag))
+        give_up();
+    if (!good) return false;
+    ph.own[0] ^= 1u;
+    if (used1) ph.own[1] ^= 1u;
+    tc_fence_after();
+    const bool flagged = flags[2 * slot + s] || (split && flags[2 * slot + (s ^ 1)]);
+    const bool whole = (x.flags & kPartWhole) != 0;
+    const long long prow =
+        static_cast<long long>(2 * c + ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows;
+    const float *m0 = tree_stats<D>(blk.smem) + kMax, *m1 = m0 + 256;
+    const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
+    // rows in turn: in a split the groups take eights (or, of up to eight
+    // rows, the rows) in turn
+    const bool by_row = split && rows <= 8;
+    const long long first_row = static_cast<long long>(x.tok) * a.q_heads + x.h * g.group;
+#pragma unroll 1
+    for (int n0 = split && !by_row ? 8 * s : 0; n0 < rows; n0 += split && !by_row ? 16 : 8) {
+        uint32_t o[8], l[8], y[8], z[8];
+        tmem_ld_32x32b_x8((split ? t0 : to) + n0, o);
+        tmem_ld_32x32b_x8((split ? t0 : to) + 32 + n0, l);
+        if (split && used1) {
+            tmem_ld_32x32b_x8(t1 + n0, y);
+            tmem_ld_32x32b_x8(t1 + 32 + n0, z);
+        }
+        tmem_ld_wait();
+        reg_fence8(o);
+        reg_fence8(l);
+        if (split && used1) {
+            reg_fence8(y);
+            reg_fence8(z);
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int r = n0 + n;
+            if (r >= rows || (by_row && (n & 1) != s)) continue;
+            float value = __uint_as_float(o[n]), sum = __uint_as_float(l[n]);
+            float top = split ? m0[r] : group_stats[kMax + r];
+            if (split && used1) {
+                const float ma = top, mb = m1[r];
+                top = fmaxf(ma, mb);
+                const float w0 = ma == -INFINITY ? 0.f : ex2((ma - top) * sc);
+                const float w1 = mb == -INFINITY ? 0.f : ex2((mb - top) * sc);
+                sum = fmaf(__uint_as_float(z[n]), w1, sum * w0);
+                value = fmaf(__uint_as_float(y[n]), w1, value * w0);
+            }
+            if (row >= D) continue;
+            if (whole) {
+                const int t = r / g.group;
+                const __nv_bfloat16 b =
+                    __float2bfloat16_rn(sum == 0.f ? 0.f : __fdividef(value, sum));
+                a.out[(first_row + static_cast<long long>(t) * a.q_heads + (r - t * g.group)) * D +
+                      row] = *reinterpret_cast<const uint16_t *>(&b);
+            } else {
+                a.partial[(prow + r) * D + row] = value;
+                if (row == 0) a.stats[prow + r] = make_float2(top, sum);
+            }
+        }
+    }
+    if (flagged && row < D) {
+        const int x0 = tree_max(x.ctx, (split ? entry.part[0].first : x.first) * kTreeTile);
+        const int x1 = tree_min(x.len, x.end * kTreeTile);
+        const long long head_step = static_cast<long long>(D) << a.page_shift;
+        const uint16_t *vc = a.v_cache + x.h * head_step + row;
+        const int *table = a.table + x.r * a.max_pages;
+        for (int r = 0; r < rows; ++r) {
+            if (split && (by_row ? r & 1 : (r >> 3) & 1) != s) continue;
+            const int t = r / g.group;
+            const TreeSight sight{
+                a.mask ? a.mask + static_cast<long long>(x.tok + t) * a.mask_words : nullptr,
+                a.mask_words, x.place + t, x.ctx, x.len};
+            if (whole)
+                tree_add_nonfinite<D>(
+                    a.out + (first_row + static_cast<long long>(t) * a.q_heads + r % g.group) * D + row,
+                    1, sight, x0, x1, table, a.page_shift, a.num_pages, g.kv_heads * head_step, vc);
+            else
+                tree_add_nonfinite<D>(a.partial + (prow + r) * D + row, 1, sight, x0, x1, table,
+                                      a.page_shift, a.num_pages, g.kv_heads * head_step, vc);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (split) {
+        if (lane == 0) mbar_arrive(bars.o_done(quad));
+        ph.merged = true;
+        ph.merge ^= 1u;
+    } else {
+        group_sync(s);   // the maxima have been read
+    }
+    return true;
+}
+
+template <int D>
+__device__ __forceinline__ void tree_softmax_narrow(const TreeAttnArgs &a, const TreeBlock &blk) {
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const int s = threadIdx.x >> 7, lane = threadIdx.x & 31;
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    const TreeEntry *entries = tree_entries<D>(blk.smem);
+    TreePhase ph{};
+    bool ok = true;
+    for (int seq = 0;; ++seq) {
+        const int slot = seq % kTreeEntries;
+        // The group's warps leave together: one that gave up comes here first,
+        // so that none is left alone at a group barrier.
+        ok = ok && warp_wait(bars.e_full(slot), (seq / kTreeEntries) & 1, abort_flag);
         if (!ok && lane == 0 && !*abort_flag) {
             atomicOr(&g_status_word, kStatusEpilogueTimeout);
             *abort_flag = 1;
         }
+        if (group_any(s, !ok) || entries[slot].steps == 0) break;
+        ok = tree_narrow_part<D>(a, blk, entries[slot], slot, ph);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bars.e_empty(slot));
+    }
+}
+
+// ---- softmax, wide form: one thread a row
+template <int D>
+__device__ __forceinline__ void tree_softmax_wide(const TreeAttnArgs &a, const TreeBlock &blk) {
+    const TreeGeom &g = a.geom;
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = warp >> 2, quad = warp & 3;
+    const int row = 32 * quad + lane;
+    const int c = static_cast<int>(blockIdx.x);
+    const int my_tok = row / g.group, my_head = row - my_tok * g.group;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t ts = blk.tmem + lanes + 128 * s;                            // scores, weights
+    const uint32_t to = blk.tmem + lanes + TreeShared<D>::TMEM_O + D * s;      // own accumulator
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    volatile int *flags = tree_flags<D>(blk.smem);
+    float2 *row_stats = reinterpret_cast<float2 *>(tree_stats<D>(blk.smem));
+    const TreeEntry *entries = tree_entries<D>(blk.smem);
+    uint32_t sphase = 0, ophase0 = 0, ophase1 = 0, xphase = 0;
+    bool ok = true, merged = false;   // merged: results were shared, o_done is due
+    for (int seq = 0;; ++seq) {
+        const int slot = seq % kTreeEntries;
+        ok = warp_wait(bars.e_full(slot), (seq / kTreeEntries) & 1, abort_flag);
+        if (!ok) break;
+        const TreeEntry &entry = entries[slot];
+        if (entry.steps == 0) break;
+        // most of it stays in shared memory: the scores need the registers
+        const TreePart &x = entry.part[s];
+        const bool warp_on = 32 * quad < x.ntok * g.group;
+        const bool row_on = my_tok < x.ntok;
+        auto sight = [&] {
+            return TreeSight{a.mask ? a.mask + static_cast<long long>(x.tok + my_tok) *
+                                                   a.mask_words
+                                    : nullptr,
+                             a.mask_words, x.place + my_tok, x.ctx, x.len};
+        };
+        // the weights' first half is in place, and the accumulator of the
+        // entry before has been read by both groups
+        auto first_half = [&] {
+            if (merged) {
+                ok = warp_wait(bars.o_done(quad), xphase ^ 1u, abort_flag) && ok;
+                merged = false;
+            }
+            if (warp_on) {
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.p_half(s));
+        };
+        float m = -INFINITY, l = 0.f;
+        bool fresh = true;
+        for (int tile = x.first; tile < x.end; tile += x.stride) {
+            ok = warp_wait(bars.s_full(s), sphase, abort_flag);
+            if (!ok) break;
+            sphase ^= 1u;
+            if (warp_on) {
+                tc_fence_after();
+                uint32_t v[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, v[i]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) reg_fence32(v[i]);
+                if (x.edge(tile)) {
+                    const TreeSight t = sight();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t see =
+                            row_on ? tree_visible(t, tile * kTreeTile + 32 * i) : 0u;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((see >> j) & 1u)) v[i][j] = 0xFF800000u;
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3],
+                                                 fmaxf(__uint_as_float(v[i][j]),
+                                                       __uint_as_float(v[i][j + 1])));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (fresh) {
+                    m = top;
+                    fresh = false;
+                } else {
+                    const bool rise = top * a.scale_log2 > m * a.scale_log2 + kTreeRescale;
+                    if (__any_sync(~0u, rise && row_on)) {
+                        const float f = rise ? ex2((m - top) * a.scale_log2) : 1.f;
+                        m = rise ? top : m;
+                        l *= f;
+#pragma unroll 1
+                        for (int i = 0; i < D / 32; ++i) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(to + 32 * i, o);
+                            tmem_ld_wait();
+                            reg_fence32(o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st_32x32b_x32(to + 32 * i, o);
+                        }
+                    }
+                }
+                // an all-masked row so far: weights 2^(-inf - 0) = 0
+                const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i == 2) {
+                        first_half();
+                    }
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float lo, hi;
+                        fma2(lo, hi, __uint_as_float(v[i][2 * j]),
+                             __uint_as_float(v[i][2 * j + 1]), a.scale_log2, base);
+                        lo = ex2(lo);
+                        hi = ex2(hi);
+                        add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
+                        p[j] = pack_bf16x2(lo, hi);
+                    }
+                    tmem_st_32x32b_x16(ts + 16 * i, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            }
+            if (!warp_on) first_half();
+            if (!ok) break;
+            if (warp_on) {
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.p_ready(s));
+        }
+        if (!ok) break;
+
+        // ---- the entry's end: this block's result
+        const bool whole = (x.flags & kPartWhole) != 0;
+        // partial results: slot 2c + 1 for an item that begins here, 2c for others
+        const long long prow =
+            static_cast<long long>(2 * c + ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows +
+            ((x.flags & kPartSecond) ? 128 : 0) + row;
+        const bool split = entry.kind == kTreeSplit;
+        const bool used1 = entry.part[1].used();
+        int first = x.first;              // this block's tiles of the item
+        float w0 = 1.f, w1 = 0.f;
+        int c0 = 0, c1 = D;               // columns that this thread writes
+        if (split) {
+            // merge the groups' statistics; each writes half of the columns
+            first = entry.part[0].first;
+            if (x.used()) row_stats[128 * s + row] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.st_ready(quad));
+            ok = warp_wait(bars.st_ready(quad), xphase, abort_flag);
+            if (!ok) break;
+            const float2 a0 = row_stats[row];
+            const float2 a1 = used1 ? row_stats[128 + row] : make_float2(-INFINITY, 0.f);
+            m = fmaxf(a0.x, a1.x);
+            w0 = a0.x == -INFINITY ? 0.f : ex2((a0.x - m) * a.scale_log2);
+            w1 = a1.x == -INFINITY ? 0.f : ex2((a1.x - m) * a.scale_log2);
+            l = a0.y * w0 + a1.y * w1;
+            c0 = s * (D / 2);
+            c1 = c0 + D / 2;
+        }
+        if (split || s == 0) ok = warp_wait(bars.o_full(0), ophase0, abort_flag);
+        if (ok && used1 && (split || s == 1)) ok = warp_wait(bars.o_full(1), ophase1, abort_flag);
+        if (!ok) break;
+        ophase0 ^= 1u;
+        if (used1) ophase1 ^= 1u;
+        tc_fence_after();
+        const bool flagged = flags[2 * slot + s] || (split && flags[2 * slot + (s ^ 1)]);
+        if (warp_on) {
+            if (!whole && row_on && (!split || s == 0)) a.stats[prow] = make_float2(m, l);
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
+#pragma unroll 1
+            for (int col = c0; col < c1; col += 32) {
+                uint32_t o[32];
+                if (!split) {
+                    tmem_ld_32x32b_x32(to + col, o);
+                    tmem_ld_wait();
+                    reg_fence32(o);
+                } else {
+                    tmem_ld_32x32b_x32(t0 + col, o);
+                    uint32_t y[32];
+                    if (used1) tmem_ld_32x32b_x32(t1 + col, y);
+                    tmem_ld_wait();
+                    reg_fence32(o);
+                    if (used1) {
+                        reg_fence32(y);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), w1,
+                                                        __uint_as_float(o[j]) * w0));
+                    }
+                }
+                if (!row_on) continue;
+                uint16_t *const out = a.out + (static_cast<long long>(x.tok + my_tok) * a.q_heads +
+                                               x.h * g.group + my_head) * D + col;
+                float *const sums = a.partial + prow * D + col;
+                if (whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(out);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t b[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            b[k] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * k]) * inv,
+                                               __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
+                        dst[j] = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(sums);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
+                if (flagged) {
+                    const int x0 = tree_max(x.ctx, first * kTreeTile);
+                    const int x1 = tree_min(x.len, x.end * kTreeTile);
+                    const long long head_step = static_cast<long long>(D) << a.page_shift;
+                    const uint16_t *vc = a.v_cache + x.h * head_step + col;
+                    const int *table = a.table + x.r * a.max_pages;
+                    if (whole)
+                        tree_add_nonfinite<D>(out, 32, sight(), x0, x1, table, a.page_shift,
+                                              a.num_pages, g.kv_heads * head_step, vc);
+                    else
+                        tree_add_nonfinite<D>(sums, 32, sight(), x0, x1, table, a.page_shift,
+                                              a.num_pages, g.kv_heads * head_step, vc);
+                }
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        if (split) {
+            if (lane == 0) mbar_arrive(bars.o_done(quad));
+            merged = true;
+            xphase ^= 1u;
+        }
+        if (lane == 0) mbar_arrive(bars.e_empty(slot));
+    }
+    if (!ok && lane == 0 && !*abort_flag) {
+        atomicOr(&g_status_word, kStatusEpilogueTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// ---- one block in one form
+template <int D, bool NARROW, typename Load>
+__device__ __forceinline__ void tree_block(const CUtensorMap &tmQ, const CUtensorMap &tmK,
+                                           const CUtensorMap &tmV, const TreeAttnArgs &a,
+                                           const TreeBlock &blk, const TreeStart &start, Load load) {
+    using C = TreeCfg<D, NARROW>;
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    uint2 issued = make_uint2(0, 0);
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeOtherRegs));
+        if (warp == 8) {
+            issued = tree_produce<D, NARROW>(tmQ, tmK, tmV, a, blk);
+        } else if (warp == 9) {
+            if (lane == 0) tree_issue<D, NARROW>(blk);
+        } else if (warp == 10) {
+            tree_mend_v<D, NARROW>(blk);
+        } else if (lane == 0) {
+            tree_describe<D>(a, blk, start, load);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftmaxRegs));
+        if constexpr (NARROW)
+            tree_softmax_narrow<D>(a, blk);
+        else
+            tree_softmax_wide<D>(a, blk);
     }
 
     // ---- teardown: every role has left its loop
@@ -873,21 +1300,167 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (warp == 8 && lane == 0) {
             // every TMA load already issued lands before shared memory is reused
             for (int i = 0; i < C::STAGES + 2; ++i)
-                if ((issued >> i) & 1u)
-                    if (!mbar_wait_drain(i < C::STAGES ? kv_full(i) : q_full(i - C::STAGES),
-                                         (parity >> i) & 1u))
+                if ((issued.x >> i) & 1u)
+                    if (!mbar_wait_drain(i < C::STAGES ? bars.kv_full(i) : bars.q_full(i - C::STAGES),
+                                         (issued.y >> i) & 1u))
                         atomicOr(&g_status_word, kStatusDrainTimeout);
         }
         if (warp == 9 && lane == 0) {
-            umma_commit(drain_bar);
-            if (!mbar_wait_drain(drain_bar, 0)) atomicOr(&g_status_word, kStatusDrainTimeout);
+            umma_commit(bars.drain());
+            if (!mbar_wait_drain(bars.drain(), 0)) atomicOr(&g_status_word, kStatusDrainTimeout);
         }
         __syncthreads();
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
+                          const __grid_constant__ CUtensorMap tmQn,
+                          const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV,
+                          const __grid_constant__ TreeAttnArgs a) {
+    using S = TreeShared<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const TreeBars<D> bars{smem_u32(smem)};
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const TreeGeom &g = a.geom;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + S::OFF_MISC);
+    TreeStart *start = reinterpret_cast<TreeStart *>(smem + S::OFF_MISC + 48);
+    // the prologue's sums, in the statistics' place
+    long long *warp_sums = reinterpret_cast<long long *>(tree_stats<D>(smem));
+
+    if (warp == 8 && lane == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(bars.kv_full(s), 1);
+            mbar_init(bars.kv_empty(s), 2);   // the MMAs' completion and warp 10
+            mbar_init(bars.v_fixed(s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bars.q_full(s), 1);
+            mbar_init(bars.q_empty(s), 1);
+            mbar_init(bars.s_full(s), 1);
+            mbar_init(bars.p_ready(s), 4);
+            mbar_init(bars.p_half(s), 4);
+            mbar_init(bars.o_full(s), 1);
+        }
+        for (int w = 0; w < 4; ++w) {
+            mbar_init(bars.st_ready(w), 2);
+            mbar_init(bars.o_done(w), 2);
+        }
+        for (int i = 0; i < kTreeEntries; ++i) {
+            mbar_init(bars.e_full(i), 1);
+            mbar_init(bars.e_empty(i), 9);    // the softmax warps and warp 10
+        }
+        mbar_init(bars.both_ready(), 8);
+        mbar_init(bars.drain(), 1);
+        *tree_abort<D>(smem) = 0;
+        start->units = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmQn);
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_holder), 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // ---- this block's share: sums over the requests, each thread a run of them
+    auto load = [&](int r) {
+        return tree_request(g, a.query_start[r], a.query_start[r + 1], a.ctx_lens[r]);
+    };
+    // a request on one form's line: none of the other form's tokens
+    auto on_line = [&](int r, bool narrow) {
+        TreeReq q = load(r);
+        if (tree_is_narrow(g, q) != narrow) q.n = 0;
+        return q;
+    };
+    TreeBlock blk{};
+    blk.smem = smem;
+    bool narrow = false;
+    {
+        const int per = (g.requests + kTreeThreads - 1) / kTreeThreads;
+        const int r0 = tree_min(static_cast<int>(threadIdx.x) * per, g.requests);
+        const int r1 = tree_min(r0 + per, g.requests);
+        long long units[2] = {0, 0};   // wide, narrow
+        for (int r = r0; r < r1; ++r) {
+            const TreeReq q = load(r);
+            const long long u = g.kv_heads * tree_head_units(g, q);
+            if (tree_is_narrow(g, q)) units[1] += u; else units[0] += u;
+        }
+        const TreeScan wide_scan = tree_block_scan(units[0], warp_sums);
+        const TreeScan narrow_scan = tree_block_scan(units[1], warp_sums + kTreeThreads / 32);
+        const long long nw = wide_scan.total, nn = narrow_scan.total;
+        const int lines = (nw > 0) + (nn > 0);
+        const int blocks = static_cast<int>(
+            max(static_cast<long long>(lines),
+                min(static_cast<long long>(gridDim.x), tree_div(nw + nn, a.min_units))));
+        const int nb = static_cast<int>(
+            min(static_cast<long long>(tree_narrow_blocks(nn, nw, blocks)), nn));
+        const int wb = static_cast<int>(min(static_cast<long long>(blocks - nb), nw));
+        const int c = static_cast<int>(blockIdx.x);
+        narrow = c < nb;
+        blk.base = narrow ? 0 : nb;
+        blk.index = c - blk.base;
+        const int mine_of = narrow ? nb : wb;
+        if (blk.index < mine_of) {
+            blk.cut = tree_cut(narrow ? nn : nw, mine_of);
+            const TreeScan scan = narrow ? narrow_scan : wide_scan;
+            const long long mine = units[narrow];
+            const long long u0 = tree_block_begin(blk.cut, blk.index);
+            if (u0 >= scan.before && u0 < scan.before + mine) {
+                long long at = scan.before;
+                for (int r = r0; r < r1; ++r) {
+                    const TreeReq q = on_line(r, narrow);
+                    const long long u = g.kv_heads * tree_head_units(g, q);
+                    if (u0 < at + u) {
+                        start->r = r;
+                        start->units = tree_block_begin(blk.cut, blk.index + 1) - u0;
+                        tree_locate(g, q, u0 - at, start);
+                        break;
+                    }
+                    at += u;
+                }
+            }
+        }
+    }
+    // rows of no request are zero
+    {
+        const int used = g.requests > 0
+                             ? tree_min(tree_max(a.query_start[g.requests], 0), g.tokens) : 0;
+        const long long per_token = static_cast<long long>(a.q_heads) * D / 8;
+        uint4 *o = reinterpret_cast<uint4 *>(a.out);
+        for (long long i = used * per_token + blockIdx.x * kTreeThreads + threadIdx.x;
+             i < g.tokens * per_token; i += static_cast<long long>(gridDim.x) * kTreeThreads)
+            o[i] = make_uint4(0, 0, 0, 0);
+    }
+    // (the sums above have passed block barriers: the address is there)
+    blk.tmem = *tmem_holder;
+    if (narrow && warp < 4) {
+        uint32_t ones[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ones[i] = 0x3F803F80u;   // BF16 pairs
+        tc_fence_after();
+        tmem_st_32x32b_x8(blk.tmem + (static_cast<uint32_t>(32 * warp) << 16) + S::TMEM_ONES, ones);
+        tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (narrow)
+        tree_block<D, true>(tmQn, tmK, tmV, a, blk, *start, [&](int r) { return on_line(r, true); });
+    else
+        tree_block<D, false>(tmQ, tmK, tmV, a, blk, *start, [&](int r) { return on_line(r, false); });
     if (warp == 9) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(blk.tmem, 512);
     }
 }
 

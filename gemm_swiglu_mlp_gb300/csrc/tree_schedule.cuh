@@ -52,6 +52,14 @@ SWIGLU_HD TreeReq tree_request(const TreeGeom &g, int start, int end, int ctx) {
     return q;
 }
 
+// Requests of up to this many rows a kv head are worked on in the kernel's
+// narrow form, the others in its wide form, by blocks of their own: each form
+// has a line of work with only its requests on it.
+constexpr int kTreeNarrow = 32;
+SWIGLU_HD bool tree_is_narrow(const TreeGeom &g, const TreeReq &q) {
+    return static_cast<long long>(q.n) * g.group <= kTreeNarrow;
+}
+
 SWIGLU_HD int tree_items(const TreeGeom &g, const TreeReq &q) {
     return (q.n + 2 * g.tpt - 1) / (2 * g.tpt);
 }
@@ -109,6 +117,22 @@ SWIGLU_HD int tree_block_of(const TreeCut &c, long long u) {
     return static_cast<int>(u < fat ? u / (c.each + 1) : c.more + (u - fat) / c.each);
 }
 
+// How many of `blocks` (>= 2 where both lines have work) blocks take the narrow form's line: in proportion to
+// the units, a wide tile counted as kTreeWideCost / 4 narrow ones (a
+// narrow tile's time is its bytes', a wide one's also its products').
+constexpr int kTreeWideCost = 6;
+SWIGLU_HD int tree_narrow_blocks(long long narrow, long long wide, int blocks) {
+    if (narrow == 0) return 0;
+    if (wide == 0) return blocks;
+    while (((narrow | wide) >> 20) != 0) {   // keep the products in 32 bits
+        narrow = (narrow + 1) >> 1;
+        wide = (wide + 1) >> 1;
+    }
+    const uint32_t a = static_cast<uint32_t>(narrow) * 4, b = static_cast<uint32_t>(wide) * kTreeWideCost;
+    const int n = static_cast<int>((static_cast<uint64_t>(a) * blocks + (a + b) / 2) / (a + b));
+    return tree_max(1, tree_min(n, blocks - 1));
+}
+
 // Where a block begins: `tile` of item (r, h, item), `units` tiles to do.
 struct TreeStart {
     int r, h, item, tile;
@@ -133,6 +157,13 @@ SWIGLU_HD void tree_locate(const TreeGeom &g, const TreeReq &q, long long rem, T
     s->tile = static_cast<int>(rem);
 }
 
+// TreePart::flags
+enum : int {
+    kPartWhole = 1,    // this block does the whole item
+    kPartBegins = 2,   // the item begins in this block
+    kPartSecond = 4,   // the item's second row tile
+};
+
 // One softmax group's part in an entry (below): a row tile and the tiles
 // first, first + stride, .. (< end) of its item.
 struct TreePart {
@@ -151,13 +182,6 @@ struct TreePart {
     // a tile with positions that need a look: new tokens, or past the end
     SWIGLU_HD bool edge(int t) const { return (t + 1) * kTreeTile > tree_min(ctx, len); }
 };
-enum : int {
-    kPartWhole = 1,    // this block does the whole item
-    kPartBegins = 2,   // the item begins in this block
-    kPartSecond = 4,   // the item's second row tile
-    kPartShared = 8,   // the other group works on the same row tile (kTreeSplit)
-};
-
 // What both groups do next. kTreeSplit: an item of one row tile, the groups
 // take its even and odd tiles and merge their results. kTreePair: an item of
 // two row tiles, one a group, over the same tiles. kTreeDuo: two short items
@@ -268,10 +292,7 @@ struct TreeWalk {
         }
         e.part[1] = e.part[0];
         e.part[1].first += 1;
-        for (int s = 0; s < 2; ++s) {
-            e.part[s].stride = 2;
-            e.part[s].flags |= kPartShared;
-        }
+        e.part[0].stride = e.part[1].stride = 2;
         e.steps = (mine + 1) / 2;
         return e;
     }
