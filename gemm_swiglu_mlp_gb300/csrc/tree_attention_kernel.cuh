@@ -1279,7 +1279,7 @@ __device__ __forceinline__ void tree_block(const CUtensorMap &tmQ, const CUtenso
         if (warp == 8) {
             issued = tree_produce<D, NARROW>(tmQ, tmK, tmV, a, blk);
         } else if (warp == 9) {
-            if (lane == 0) tree_issue<D, NARROW>(blk);
+            if (elect_one()) tree_issue<D, NARROW>(blk);
         } else if (warp == 10) {
             tree_mend_v<D, NARROW>(blk);
         } else if (lane == 0) {
@@ -1305,7 +1305,7 @@ __device__ __forceinline__ void tree_block(const CUtensorMap &tmQ, const CUtenso
                                          (issued.y >> i) & 1u))
                         atomicOr(&g_status_word, kStatusDrainTimeout);
         }
-        if (warp == 9 && lane == 0) {
+        if (warp == 9 && elect_one()) {   // (the same lane again)
             umma_commit(bars.drain());
             if (!mbar_wait_drain(bars.drain(), 0)) atomicOr(&g_status_word, kStatusDrainTimeout);
         }
