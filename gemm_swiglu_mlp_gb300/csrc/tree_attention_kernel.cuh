@@ -12,25 +12,25 @@
 // One persistent block per SM works through its share of the line of tiles
 // (tree_schedule.cuh). All query heads of a kv head and many tokens fill the
 // 128 rows of a row tile, so each K and V tile is read once for up to two row
-// tiles. Roles (12 warps):
-//   warps 0-3, 4-7  softmax groups 0 and 1 (below)
-//   warp 8          TMA loads: K and V tiles of 128 positions, one box a page,
-//                   through one ring of stages in the order of their use
-//   warp 9          issues the MMAs
-//   warp 10         tiles with new tokens or past a request's end: zeroes V rows
-//                   past the end and takes NaN and Inf out of new tokens' V
-//                   (0 x NaN would reach rows that do not see them; the rows
-//                   that do get them back at the end)
-//   warp 11         describes the block's entries (tree_schedule.cuh) ahead of
-//                   their use, in a small ring that the other roles read
+// tiles. Roles (20 warps):
+//   warps 0-7, 8-15  softmax groups 0 and 1 (below)
+//   warp 16          TMA loads: K and V tiles of 128 positions, one box a page,
+//                    through one ring of stages in the order of their use
+//   warp 17          issues the MMAs
+//   warp 18          tiles with new tokens or past a request's end: zeroes V rows
+//                    past the end and takes NaN and Inf out of new tokens' V
+//                    (0 x NaN would reach rows that do not see them; the rows
+//                    that do get them back at the end)
+//   warp 19          describes the block's entries (tree_schedule.cuh) ahead of
+//                    their use, in a small ring that the other roles read
 //
 // Two forms, by the rows of a request and kv head (tokens x heads), each with
 // blocks of its own (tree_schedule.cuh):
-//   wide  S = Q K^T with the rows on the 128-row side (TMEM
-//       lanes), one thread a row: no exchange between threads. The weights go
-//       back to TMEM, over the scores, as the A operand of O += P V (V as it
-//       lies, MN-major), in two halves, so that the product begins while the
-//       second half's exponentials are computed.
+//   wide  S = Q K^T with the rows on the 128-row side (TMEM lanes), two
+//       threads a row, 64 positions each. They share the row's maximum; a vote
+//       per tile says whether any row of the group has outgrown its own, and
+//       only then is it exchanged. The weights go back to TMEM, over the scores,
+//       as the A operand of O += P V (V as it lies, MN-major).
 //   narrow (up to 32 rows: single tokens, small trees)  S^T = K Q^T with the
 //       positions on the 128-row side, one thread a position: a thread has
 //       as many exponentials as there are rows, where the wide form would
@@ -43,8 +43,8 @@
 // TMEM: scores of the two groups in columns 0-255, the two accumulators in
 // 256 + D each (narrow: sums of p v in 32 columns, sums of p in 32). While one group's softmax runs, the tensor cores work for the
 // other; how an entry gives both groups work is said at TreeEntry.
-// Every wait is bounded (sm103_ptx.cuh); the narrow form's group barriers are
-// reached by all four warps of a group whatever their waits said.
+// Every wait is bounded (sm103_ptx.cuh); a group's barriers are reached by all
+// of its warps whatever their waits said.
 #pragma once
 
 #include "epilogue.cuh"
@@ -71,10 +71,8 @@ struct TreeAttnArgs {
 };
 
 constexpr int kTreeEntries = 4;   // entries described ahead of their results
-constexpr int kTreeThreads = 384;
-// Registers a thread after the split: the softmax groups hold a row of 128
-// scores; 2 * 128 threads of 200 and 128 of 104 are the 384 * 168 of the launch.
-constexpr int kTreeSoftmaxRegs = 200, kTreeOtherRegs = 104;
+constexpr int kTreeThreads = 640;
+constexpr int kTreeGroup = 256;   // threads of a softmax group
 
 // Shared memory of a block, for either form.
 template <int D, bool NARROW>
@@ -105,9 +103,9 @@ struct TreeShared {
     static constexpr int OFF_BAR = OFF_ENTRY + kTreeEntries * static_cast<int>(sizeof(TreeEntry));
     static constexpr int STAGES = 11;                       // the most a form has
     // ring: full, empty, V fixed; two Q buffers: full, empty; a group: scores,
-    // weights, result, half of the weights; a warp pair: statistics, results
-    // read; entries: full, empty; both groups' statistics (narrow); drain
-    static constexpr int NUM_BARS = 3 * STAGES + 4 + 8 + 8 + 2 * kTreeEntries + 2;
+    // weights, result; entries: full, empty; both groups: statistics, results
+    // read; drain
+    static constexpr int NUM_BARS = 3 * STAGES + 4 + 6 + 2 * kTreeEntries + 3;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 80;
     static constexpr int TMEM_O = 256;
@@ -129,13 +127,11 @@ struct TreeBars {
     __device__ uint32_t s_full(int s) const { return at(3 * S::STAGES + 4 + s); }
     __device__ uint32_t p_ready(int s) const { return at(3 * S::STAGES + 6 + s); }
     __device__ uint32_t o_full(int s) const { return at(3 * S::STAGES + 8 + s); }
-    __device__ uint32_t p_half(int s) const { return at(3 * S::STAGES + 10 + s); }
-    __device__ uint32_t st_ready(int w) const { return at(3 * S::STAGES + 12 + w); }
-    __device__ uint32_t o_done(int w) const { return at(3 * S::STAGES + 16 + w); }
-    __device__ uint32_t e_full(int i) const { return at(3 * S::STAGES + 20 + i); }
-    __device__ uint32_t e_empty(int i) const { return at(3 * S::STAGES + 20 + kTreeEntries + i); }
-    __device__ uint32_t both_ready() const { return at(3 * S::STAGES + 20 + 2 * kTreeEntries); }
-    __device__ uint32_t drain() const { return at(3 * S::STAGES + 21 + 2 * kTreeEntries); }
+    __device__ uint32_t e_full(int i) const { return at(3 * S::STAGES + 10 + i); }
+    __device__ uint32_t e_empty(int i) const { return at(3 * S::STAGES + 10 + kTreeEntries + i); }
+    __device__ uint32_t both_ready() const { return at(3 * S::STAGES + 10 + 2 * kTreeEntries); }
+    __device__ uint32_t o_done() const { return at(3 * S::STAGES + 11 + 2 * kTreeEntries); }
+    __device__ uint32_t drain() const { return at(3 * S::STAGES + 12 + 2 * kTreeEntries); }
 };
 
 // The block's share of one form's line, and where things lie.
@@ -267,19 +263,19 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
     return __all_sync(~0u, mbar_wait(bar, parity, abort_flag));
 }
 
-// Barriers over the four warps of softmax group s (named barriers 1 and 2).
+// Barriers over the eight warps of softmax group s (named barriers 1 and 2).
 __device__ __forceinline__ void group_sync(int s) {
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + s), "n"(kTreeGroup) : "memory");
 }
 __device__ __forceinline__ bool group_any(int s, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %2, 0;\n\t"
-        "bar.red.or.pred q, %1, 128, p;\n\t"
+        "bar.red.or.pred q, %1, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(1 + s), "r"(static_cast<uint32_t>(v))
+        : "r"(1 + s), "r"(static_cast<uint32_t>(v)), "n"(kTreeGroup)
         : "memory");
     return r != 0;
 }
@@ -520,10 +516,10 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                                               D == 128 ? 1024 : 0, C::GROUP);
                 const uint32_t acc = blk.tmem + TreeShared<D>::TMEM_O + D * s;
                 constexpr uint32_t kstep = 2 * C::GROUP >> 4;   // 16 positions of V
+                ok = ok && mbar_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
                 if constexpr (NARROW) {
-                    ok = ok && mbar_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
                     const uint64_t wd =
                         smem_desc(sbase + C::OFF_W + s * C::W_BYTES, 16, 512, 4);
 #pragma unroll
@@ -535,20 +531,10 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                         umma_bf16_ts(acc + 32, blk.tmem + TreeShared<D>::TMEM_ONES, wd + 64u * i,
                                      idesc_l, k.step != 0 || i != 0);
                 } else {
-                    ok = ok && mbar_wait(bars.p_half(s), (pphase >> s) & 1u, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < kTreeTile / 32; ++i)
-                        umma_bf16_ts(acc, blk.tmem + 128 * s + 8 * i, vd + kstep * i,
-                                     idesc_o, k.step != 0 || i != 0);
-                    ok = mbar_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int i = kTreeTile / 32; i < kTreeTile / 16; ++i)
-                        umma_bf16_ts(acc, blk.tmem + 128 * s + 8 * i, vd + kstep * i,
-                                     idesc_o, 1u);
+                    for (int i = 0; i < kTreeTile / 16; ++i)
+                        umma_bf16_ts(acc, blk.tmem + 128 * s + 64 * (i >> 2) + 8 * (i & 3),
+                                     vd + kstep * i, idesc_o, k.step != 0 || i != 0);
                 }
                 pphase ^= 1u << s;
                 if (s == 1 || k.cur.two_kv()) umma_commit(bars.kv_empty(vstage));
@@ -707,15 +693,12 @@ struct TreePhase {
     bool merged;                            // the entry before was shared: o_done is due
 };
 
-// The entry before, if the groups shared it: all eight warps have read its
+// The entry before, if the groups shared it: all warps of both have read its
 // statistics and accumulators.
 template <int D>
 __device__ __forceinline__ bool tree_results_read(const TreeBars<D> &bars, TreePhase &ph,
                                                   const volatile int *abort_flag) {
-    bool read = true;
-    if (ph.merged)
-        for (int q = 0; q < 4; ++q)
-            read = read && warp_wait(bars.o_done(q), ph.merge ^ 1u, abort_flag);
+    const bool read = !ph.merged || warp_wait(bars.o_done(), ph.merge ^ 1u, abort_flag);
     ph.merged = false;
     return read;
 }
@@ -740,7 +723,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
     const TreeGeom &g = a.geom;
     const TreeBars<D> bars{smem_u32(blk.smem)};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = warp >> 2, quad = warp & 3;
+    const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
     const int row = 32 * quad + lane;
     const int c = static_cast<int>(blockIdx.x);
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
@@ -769,7 +752,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
         good = false;
     };
     if (!tree_results_read<D>(bars, ph, abort_flag)) give_up();
-    if (quad == 0) {
+    if (warp == 8 * s) {
         group_stats[kMax + lane] = -INFINITY;
         group_stats[kAdd + lane] = kNoMax;
     }
@@ -812,7 +795,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
             // weights by the maximum so far, as if no score had outgrown it
             bool rise = false;
 #pragma unroll 1
-            for (int n0 = 0; n0 < rows && good; n0 += 8) {
+            for (int n0 = 8 * half; n0 < rows && good; n0 += 16) {
                 uint32_t v[8];
                 scores(n0, v);
                 float add[8];
@@ -838,7 +821,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
             if (!risen) break;
             // new maxima: each warp's, then the group's
 #pragma unroll 1
-            for (int n0 = 0; n0 < rows && good; n0 += 8) {
+            for (int n0 = 8 * half; n0 < rows && good; n0 += 16) {
                 uint32_t v[8];
                 scores(n0, v);
                 float top[8];
@@ -851,7 +834,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
                 }
             }
             group_sync(s);
-            if (quad == 0 && lane < rows) {
+            if (warp == 8 * s && lane < rows) {
                 const float old = group_stats[kMax + lane];
                 const float top = fmaxf(fmaxf(fmaxf(group_stats[lane], group_stats[32 + lane]),
                                               fmaxf(group_stats[64 + lane], group_stats[96 + lane])),
@@ -864,7 +847,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
             if (!first && tile != x.first) {
                 // the sums of p v (columns 0 - 31) and of p (32 - 63)
 #pragma unroll 1
-                for (int n0 = 0; n0 < rows && good; n0 += 8) {
+                for (int n0 = 8 * half; n0 < rows && good; n0 += 16) {
                     uint32_t o[8], l[8];
                     tmem_ld_32x32b_x8(to + n0, o);
                     tmem_ld_32x32b_x8(to + 32 + n0, l);
@@ -910,12 +893,13 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
         static_cast<long long>(2 * c + ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows;
     const float *m0 = tree_stats<D>(blk.smem) + kMax, *m1 = m0 + 256;
     const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
-    // rows in turn: in a split the groups take eights (or, of up to eight
-    // rows, the rows) in turn
-    const bool by_row = split && rows <= 8;
+    // the halves of a group, in a split all four, take eights of rows in turn;
+    // with up to eight rows the rows
+    const int turns = split ? 4 : 2, turn = split ? 2 * s + half : half;
+    const bool by_row = rows <= 8;
     const long long first_row = static_cast<long long>(x.tok) * a.q_heads + x.h * g.group;
 #pragma unroll 1
-    for (int n0 = split && !by_row ? 8 * s : 0; n0 < rows; n0 += split && !by_row ? 16 : 8) {
+    for (int n0 = by_row ? 0 : 8 * turn; n0 < rows; n0 += by_row ? 8 : 8 * turns) {
         uint32_t o[8], l[8], y[8], z[8];
         tmem_ld_32x32b_x8((split ? t0 : to) + n0, o);
         tmem_ld_32x32b_x8((split ? t0 : to) + 32 + n0, l);
@@ -933,7 +917,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const int r = n0 + n;
-            if (r >= rows || (by_row && (n & 1) != s)) continue;
+            if (r >= rows || (by_row && (n & (turns - 1)) != turn)) continue;
             float value = __uint_as_float(o[n]), sum = __uint_as_float(l[n]);
             float top = split ? m0[r] : group_stats[kMax + r];
             if (split && used1) {
@@ -964,7 +948,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
         const uint16_t *vc = a.v_cache + x.h * head_step + row;
         const int *table = a.table + x.r * a.max_pages;
         for (int r = 0; r < rows; ++r) {
-            if (split && (by_row ? r & 1 : (r >> 3) & 1) != s) continue;
+            if (((by_row ? r : r >> 3) & (turns - 1)) != turn) continue;
             const int t = r / g.group;
             const TreeSight sight{
                 a.mask ? a.mask + static_cast<long long>(x.tok + t) * a.mask_words : nullptr,
@@ -981,7 +965,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
     tc_fence_before();
     __syncwarp();
     if (split) {
-        if (lane == 0) mbar_arrive(bars.o_done(quad));
+        if (lane == 0) mbar_arrive(bars.o_done());
         ph.merged = true;
         ph.merge ^= 1u;
     } else {
@@ -990,10 +974,259 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
     return true;
 }
 
+// ---- softmax, wide form. One entry's part, for the warps of one group: a
+// thread is a row and half of each tile's positions. As tree_narrow_part.
 template <int D>
-__device__ __forceinline__ void tree_softmax_narrow(const TreeAttnArgs &a, const TreeBlock &blk) {
+__device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const TreeBlock &blk,
+                                               const TreeEntry &entry, int slot, TreePhase &ph) {
+    const TreeGeom &g = a.geom;
     const TreeBars<D> bars{smem_u32(blk.smem)};
-    const int s = threadIdx.x >> 7, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+    const int row = 32 * quad + lane;
+    const int my_tok = row / g.group;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t ts = blk.tmem + lanes + 128 * s;                            // scores, weights
+    const uint32_t to = blk.tmem + lanes + TreeShared<D>::TMEM_O + D * s;      // own accumulator
+    volatile int *abort_flag = tree_abort<D>(blk.smem);
+    volatile int *flags = tree_flags<D>(blk.smem);
+    // rows' statistics: the halves' maxima, at the end the maximum and the sum
+    float2 *stats = reinterpret_cast<float2 *>(tree_stats<D>(blk.smem)) + 128 * s;
+    const TreePart &x = entry.part[s];
+    const bool split = entry.kind == kTreeSplit;
+    const bool warp_on = 32 * quad < x.ntok * g.group;
+    const bool row_on = my_tok < x.ntok;
+    const float sc = a.scale_log2;
+    bool good = true;
+    auto give_up = [&] {
+        if (lane == 0 && !*abort_flag) {
+            atomicOr(&g_status_word, kStatusEpilogueTimeout);
+            *abort_flag = 1;
+        }
+        good = false;
+    };
+    auto sight = [&] {
+        return TreeSight{
+            a.mask ? a.mask + static_cast<long long>(x.tok + my_tok) * a.mask_words : nullptr,
+            a.mask_words, x.place + my_tok, x.ctx, x.len};
+    };
+    if (!tree_results_read<D>(bars, ph, abort_flag)) give_up();
+    float m = -INFINITY, l = 0.f;
+    for (int tile = x.first; tile < x.end; tile += x.stride) {
+        if (good && !warp_wait(bars.s_full(s), ph.scores, abort_flag)) give_up();
+        ph.scores ^= 1u;
+        tc_fence_after();
+        const bool fresh = tile == x.first;
+        // the 64 scores, 32 at a time, twice: first their maximum, then the
+        // weights (kept meanwhile they would be most of a thread's registers)
+        uint32_t see[2] = {~0u, ~0u};
+        if (x.edge(tile)) {
+            const TreeSight t = sight();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                see[i] = row_on ? tree_visible(t, tile * kTreeTile + 64 * half + 32 * i) : 0u;
+        }
+        auto scores = [&](int i, uint32_t (&v)[32]) {
+            tmem_ld_32x32b_x32(ts + 64 * half + 32 * i, v);
+            tmem_ld_wait();
+            reg_fence32(v);
+            if (see[i] != ~0u) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (!((see[i] >> j) & 1u)) v[j] = 0xFF800000u;
+            }
+        };
+        float top = -INFINITY;
+        if (warp_on) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t v[32];
+                scores(i, v);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3], fmaxf(__uint_as_float(v[j]),
+                                                                     __uint_as_float(v[j + 1])));
+            }
+            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        }
+        const bool rise = fresh || (row_on && top * sc > m * sc + kTreeRescale);
+        const bool risen = group_any(s, rise && good);
+        if (*abort_flag) good = false;
+        if (risen) {
+            if (half) stats[row].y = top; else stats[row].x = top;
+            group_sync(s);
+            const float2 both = stats[row];
+            const float now = fmaxf(both.x, both.y);
+            float f = 1.f;
+            if (now > m && (fresh || now * sc > m * sc + kTreeRescale)) {
+                f = ex2((m - now) * sc);
+                m = now;
+                l *= f;
+            }
+            if (!fresh && warp_on && __any_sync(~0u, row_on && f != 1.f)) {
+#pragma unroll 1
+                for (int col = half * (D / 2); col < (half + 1) * (D / 2); col += 16) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(to + col, o);
+                    tmem_ld_wait();
+                    reg_fence16(o);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st_32x32b_x16(to + col, o);
+                }
+            }
+        }
+        if (warp_on) {
+            // no maximum so far: weights 2^(-inf - 0) = 0
+            const float base = m == -INFINITY ? 0.f : -m * sc;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t v[32], p[16];
+                scores(i, v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float lo, hi;
+                    fma2(lo, hi, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), sc, base);
+                    lo = ex2(lo);
+                    hi = ex2(hi);
+                    add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
+                    p[j] = pack_bf16x2(lo, hi);
+                }
+                // over this half's own scores, those read already
+                tmem_st_32x32b_x16(ts + 64 * half + 16 * i, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tc_fence_before();
+        }
+        __syncwarp();
+        if (good && lane == 0) mbar_arrive(bars.p_ready(s));
+    }
+
+    // ---- this block's result: the rows' sums, then (split) the other group's
+    group_sync(s);   // (the last maxima have been read)
+    if (half) stats[row].y = l;
+    group_sync(s);
+    if (!half) stats[row] = make_float2(m, l + stats[row].y);
+    if (split) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.both_ready());
+        if (good && !warp_wait(bars.both_ready(), ph.both, abort_flag)) give_up();
+        ph.both ^= 1u;
+    } else {
+        group_sync(s);
+        if (*abort_flag) good = false;
+    }
+    const bool used1 = entry.part[1].used();
+    if (good && (split || s == 0) && !warp_wait(bars.o_full(0), ph.own[0], abort_flag)) give_up();
+    if (good && used1 && (split || s == 1) && !warp_wait(bars.o_full(1), ph.own[1], abort_flag))
+        give_up();
+    if (!good) return false;
+    ph.own[0] ^= 1u;
+    if (used1) ph.own[1] ^= 1u;
+    tc_fence_after();
+    if (warp_on) {
+        const bool flagged = flags[2 * slot + s] || (split && flags[2 * slot + (s ^ 1)]);
+        const bool whole = (x.flags & kPartWhole) != 0;
+        // partial results: slot 2c + 1 for an item that begins here, 2c for others
+        const long long prow =
+            static_cast<long long>(2 * static_cast<int>(blockIdx.x) +
+                                   ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows +
+            ((x.flags & kPartSecond) ? 128 : 0) + row;
+        float2 st = stats[row];
+        float w0 = 1.f, w1 = 0.f;
+        if (split) {
+            const float2 *all = reinterpret_cast<const float2 *>(tree_stats<D>(blk.smem));
+            const float2 a0 = all[row];
+            const float2 a1 = used1 ? all[128 + row] : make_float2(-INFINITY, 0.f);
+            const float top = fmaxf(a0.x, a1.x);
+            w0 = a0.x == -INFINITY ? 0.f : ex2((a0.x - top) * sc);
+            w1 = a1.x == -INFINITY ? 0.f : ex2((a1.x - top) * sc);
+            st = make_float2(top, a0.y * w0 + a1.y * w1);
+        }
+        if (!whole && row_on && half == 0 && (!split || s == 0)) a.stats[prow] = st;
+        const float inv = whole ? (st.y == 0.f ? 0.f : 1.f / st.y) : 1.f;
+        const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
+        // this thread's columns: its half of the row, in a split its quarter
+        const int width = split ? D / 4 : D / 2;
+        const int c0 = (split ? 2 * s + half : half) * width;
+        uint16_t *const out = a.out + (static_cast<long long>(x.tok + my_tok) * a.q_heads +
+                                       x.h * g.group + (row - my_tok * g.group)) * D;
+        float *const sums = a.partial + prow * D;
+#pragma unroll 1
+        for (int col = c0; col < c0 + width; col += 16) {
+            uint32_t o[16];
+            if (!split) {
+                tmem_ld_32x32b_x16(to + col, o);
+                tmem_ld_wait();
+                reg_fence16(o);
+            } else {
+                tmem_ld_32x32b_x16(t0 + col, o);
+                uint32_t y[16];
+                if (used1) tmem_ld_32x32b_x16(t1 + col, y);
+                tmem_ld_wait();
+                reg_fence16(o);
+                if (used1) {
+                    reg_fence16(y);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), w1,
+                                                    __uint_as_float(o[j]) * w0));
+                }
+            }
+            if (!row_on) continue;
+            if (whole) {
+                uint4 *dst = reinterpret_cast<uint4 *>(out + col);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t b[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        b[i] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * i]) * inv,
+                                           __uint_as_float(o[8 * j + 2 * i + 1]) * inv);
+                    dst[j] = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(sums + col);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+        }
+        if (flagged && row_on) {
+            const int x0 = tree_max(x.ctx, (split ? entry.part[0].first : x.first) * kTreeTile);
+            const int x1 = tree_min(x.len, x.end * kTreeTile);
+            const long long head_step = static_cast<long long>(D) << a.page_shift;
+            const uint16_t *vc = a.v_cache + x.h * head_step + c0;
+            const int *table = a.table + x.r * a.max_pages;
+            if (whole)
+                tree_add_nonfinite<D>(out + c0, width, sight(), x0, x1, table, a.page_shift,
+                                      a.num_pages, g.kv_heads * head_step, vc);
+            else
+                tree_add_nonfinite<D>(sums + c0, width, sight(), x0, x1, table, a.page_shift,
+                                      a.num_pages, g.kv_heads * head_step, vc);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (split) {
+        if (lane == 0) mbar_arrive(bars.o_done());
+        ph.merged = true;
+        ph.merge ^= 1u;
+    } else {
+        group_sync(s);   // the sums have been read
+    }
+    return true;
+}
+
+// ---- the softmax warps of one group, entry by entry
+template <int D, bool NARROW>
+__device__ __forceinline__ void tree_softmax(const TreeAttnArgs &a, const TreeBlock &blk) {
+    const TreeBars<D> bars{smem_u32(blk.smem)};
+    const int s = threadIdx.x / kTreeGroup, lane = threadIdx.x & 31;
     volatile int *abort_flag = tree_abort<D>(blk.smem);
     const TreeEntry *entries = tree_entries<D>(blk.smem);
     TreePhase ph{};
@@ -1008,259 +1241,10 @@ __device__ __forceinline__ void tree_softmax_narrow(const TreeAttnArgs &a, const
             *abort_flag = 1;
         }
         if (group_any(s, !ok) || entries[slot].steps == 0) break;
-        ok = tree_narrow_part<D>(a, blk, entries[slot], slot, ph);
+        ok = NARROW ? tree_narrow_part<D>(a, blk, entries[slot], slot, ph)
+                    : tree_wide_part<D>(a, blk, entries[slot], slot, ph);
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bars.e_empty(slot));
-    }
-}
-
-// ---- softmax, wide form: one thread a row
-template <int D>
-__device__ __forceinline__ void tree_softmax_wide(const TreeAttnArgs &a, const TreeBlock &blk) {
-    const TreeGeom &g = a.geom;
-    const TreeBars<D> bars{smem_u32(blk.smem)};
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = warp >> 2, quad = warp & 3;
-    const int row = 32 * quad + lane;
-    const int c = static_cast<int>(blockIdx.x);
-    const int my_tok = row / g.group, my_head = row - my_tok * g.group;
-    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t ts = blk.tmem + lanes + 128 * s;                            // scores, weights
-    const uint32_t to = blk.tmem + lanes + TreeShared<D>::TMEM_O + D * s;      // own accumulator
-    volatile int *abort_flag = tree_abort<D>(blk.smem);
-    volatile int *flags = tree_flags<D>(blk.smem);
-    float2 *row_stats = reinterpret_cast<float2 *>(tree_stats<D>(blk.smem));
-    const TreeEntry *entries = tree_entries<D>(blk.smem);
-    uint32_t sphase = 0, ophase0 = 0, ophase1 = 0, xphase = 0;
-    bool ok = true, merged = false;   // merged: results were shared, o_done is due
-    for (int seq = 0;; ++seq) {
-        const int slot = seq % kTreeEntries;
-        ok = warp_wait(bars.e_full(slot), (seq / kTreeEntries) & 1, abort_flag);
-        if (!ok) break;
-        const TreeEntry &entry = entries[slot];
-        if (entry.steps == 0) break;
-        // most of it stays in shared memory: the scores need the registers
-        const TreePart &x = entry.part[s];
-        const bool warp_on = 32 * quad < x.ntok * g.group;
-        const bool row_on = my_tok < x.ntok;
-        auto sight = [&] {
-            return TreeSight{a.mask ? a.mask + static_cast<long long>(x.tok + my_tok) *
-                                                   a.mask_words
-                                    : nullptr,
-                             a.mask_words, x.place + my_tok, x.ctx, x.len};
-        };
-        // the weights' first half is in place, and the accumulator of the
-        // entry before has been read by both groups
-        auto first_half = [&] {
-            if (merged) {
-                ok = warp_wait(bars.o_done(quad), xphase ^ 1u, abort_flag) && ok;
-                merged = false;
-            }
-            if (warp_on) {
-                tmem_st_wait();
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.p_half(s));
-        };
-        float m = -INFINITY, l = 0.f;
-        bool fresh = true;
-        for (int tile = x.first; tile < x.end; tile += x.stride) {
-            ok = warp_wait(bars.s_full(s), sphase, abort_flag);
-            if (!ok) break;
-            sphase ^= 1u;
-            if (warp_on) {
-                tc_fence_after();
-                uint32_t v[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, v[i]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) reg_fence32(v[i]);
-                if (x.edge(tile)) {
-                    const TreeSight t = sight();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t see =
-                            row_on ? tree_visible(t, tile * kTreeTile + 32 * i) : 0u;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((see >> j) & 1u)) v[i][j] = 0xFF800000u;
-                    }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3],
-                                                 fmaxf(__uint_as_float(v[i][j]),
-                                                       __uint_as_float(v[i][j + 1])));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (fresh) {
-                    m = top;
-                    fresh = false;
-                } else {
-                    const bool rise = top * a.scale_log2 > m * a.scale_log2 + kTreeRescale;
-                    if (__any_sync(~0u, rise && row_on)) {
-                        const float f = rise ? ex2((m - top) * a.scale_log2) : 1.f;
-                        m = rise ? top : m;
-                        l *= f;
-#pragma unroll 1
-                        for (int i = 0; i < D / 32; ++i) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32(to + 32 * i, o);
-                            tmem_ld_wait();
-                            reg_fence32(o);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st_32x32b_x32(to + 32 * i, o);
-                        }
-                    }
-                }
-                // an all-masked row so far: weights 2^(-inf - 0) = 0
-                const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i == 2) {
-                        first_half();
-                    }
-                    uint32_t p[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float lo, hi;
-                        fma2(lo, hi, __uint_as_float(v[i][2 * j]),
-                             __uint_as_float(v[i][2 * j + 1]), a.scale_log2, base);
-                        lo = ex2(lo);
-                        hi = ex2(hi);
-                        add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
-                        p[j] = pack_bf16x2(lo, hi);
-                    }
-                    tmem_st_32x32b_x16(ts + 16 * i, p);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            }
-            if (!warp_on) first_half();
-            if (!ok) break;
-            if (warp_on) {
-                tmem_st_wait();
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.p_ready(s));
-        }
-        if (!ok) break;
-
-        // ---- the entry's end: this block's result
-        const bool whole = (x.flags & kPartWhole) != 0;
-        // partial results: slot 2c + 1 for an item that begins here, 2c for others
-        const long long prow =
-            static_cast<long long>(2 * c + ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows +
-            ((x.flags & kPartSecond) ? 128 : 0) + row;
-        const bool split = entry.kind == kTreeSplit;
-        const bool used1 = entry.part[1].used();
-        int first = x.first;              // this block's tiles of the item
-        float w0 = 1.f, w1 = 0.f;
-        int c0 = 0, c1 = D;               // columns that this thread writes
-        if (split) {
-            // merge the groups' statistics; each writes half of the columns
-            first = entry.part[0].first;
-            if (x.used()) row_stats[128 * s + row] = make_float2(m, l);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.st_ready(quad));
-            ok = warp_wait(bars.st_ready(quad), xphase, abort_flag);
-            if (!ok) break;
-            const float2 a0 = row_stats[row];
-            const float2 a1 = used1 ? row_stats[128 + row] : make_float2(-INFINITY, 0.f);
-            m = fmaxf(a0.x, a1.x);
-            w0 = a0.x == -INFINITY ? 0.f : ex2((a0.x - m) * a.scale_log2);
-            w1 = a1.x == -INFINITY ? 0.f : ex2((a1.x - m) * a.scale_log2);
-            l = a0.y * w0 + a1.y * w1;
-            c0 = s * (D / 2);
-            c1 = c0 + D / 2;
-        }
-        if (split || s == 0) ok = warp_wait(bars.o_full(0), ophase0, abort_flag);
-        if (ok && used1 && (split || s == 1)) ok = warp_wait(bars.o_full(1), ophase1, abort_flag);
-        if (!ok) break;
-        ophase0 ^= 1u;
-        if (used1) ophase1 ^= 1u;
-        tc_fence_after();
-        const bool flagged = flags[2 * slot + s] || (split && flags[2 * slot + (s ^ 1)]);
-        if (warp_on) {
-            if (!whole && row_on && (!split || s == 0)) a.stats[prow] = make_float2(m, l);
-            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
-#pragma unroll 1
-            for (int col = c0; col < c1; col += 32) {
-                uint32_t o[32];
-                if (!split) {
-                    tmem_ld_32x32b_x32(to + col, o);
-                    tmem_ld_wait();
-                    reg_fence32(o);
-                } else {
-                    tmem_ld_32x32b_x32(t0 + col, o);
-                    uint32_t y[32];
-                    if (used1) tmem_ld_32x32b_x32(t1 + col, y);
-                    tmem_ld_wait();
-                    reg_fence32(o);
-                    if (used1) {
-                        reg_fence32(y);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), w1,
-                                                        __uint_as_float(o[j]) * w0));
-                    }
-                }
-                if (!row_on) continue;
-                uint16_t *const out = a.out + (static_cast<long long>(x.tok + my_tok) * a.q_heads +
-                                               x.h * g.group + my_head) * D + col;
-                float *const sums = a.partial + prow * D + col;
-                if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(out);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t b[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            b[k] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * k]) * inv,
-                                               __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
-                        dst[j] = make_uint4(b[0], b[1], b[2], b[3]);
-                    }
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(sums);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                }
-                if (flagged) {
-                    const int x0 = tree_max(x.ctx, first * kTreeTile);
-                    const int x1 = tree_min(x.len, x.end * kTreeTile);
-                    const long long head_step = static_cast<long long>(D) << a.page_shift;
-                    const uint16_t *vc = a.v_cache + x.h * head_step + col;
-                    const int *table = a.table + x.r * a.max_pages;
-                    if (whole)
-                        tree_add_nonfinite<D>(out, 32, sight(), x0, x1, table, a.page_shift,
-                                              a.num_pages, g.kv_heads * head_step, vc);
-                    else
-                        tree_add_nonfinite<D>(sums, 32, sight(), x0, x1, table, a.page_shift,
-                                              a.num_pages, g.kv_heads * head_step, vc);
-                }
-            }
-            tc_fence_before();
-        }
-        __syncwarp();
-        if (split) {
-            if (lane == 0) mbar_arrive(bars.o_done(quad));
-            merged = true;
-            xphase ^= 1u;
-        }
-        if (lane == 0) mbar_arrive(bars.e_empty(slot));
-    }
-    if (!ok && lane == 0 && !*abort_flag) {
-        atomicOr(&g_status_word, kStatusEpilogueTimeout);
-        *abort_flag = 1;
     }
 }
 
@@ -1274,30 +1258,23 @@ __device__ __forceinline__ void tree_block(const CUtensorMap &tmQ, const CUtenso
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = tree_abort<D>(blk.smem);
     uint2 issued = make_uint2(0, 0);
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeOtherRegs));
-        if (warp == 8) {
-            issued = tree_produce<D, NARROW>(tmQ, tmK, tmV, a, blk);
-        } else if (warp == 9) {
-            if (elect_one()) tree_issue<D, NARROW>(blk);
-        } else if (warp == 10) {
-            tree_mend_v<D, NARROW>(blk);
-        } else if (lane == 0) {
-            tree_describe<D>(a, blk, start, load);
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftmaxRegs));
-        if constexpr (NARROW)
-            tree_softmax_narrow<D>(a, blk);
-        else
-            tree_softmax_wide<D>(a, blk);
+    if (warp < 16) {
+        tree_softmax<D, NARROW>(a, blk);
+    } else if (warp == 16) {
+        issued = tree_produce<D, NARROW>(tmQ, tmK, tmV, a, blk);
+    } else if (warp == 17) {
+        if (elect_one()) tree_issue<D, NARROW>(blk);
+    } else if (warp == 18) {
+        tree_mend_v<D, NARROW>(blk);
+    } else if (lane == 0) {
+        tree_describe<D>(a, blk, start, load);
     }
 
     // ---- teardown: every role has left its loop
     __syncwarp();
     __syncthreads();
     if (*abort_flag) {
-        if (warp == 8 && lane == 0) {
+        if (warp == 16 && lane == 0) {
             // every TMA load already issued lands before shared memory is reused
             for (int i = 0; i < C::STAGES + 2; ++i)
                 if ((issued.x >> i) & 1u)
@@ -1305,7 +1282,7 @@ __device__ __forceinline__ void tree_block(const CUtensorMap &tmQ, const CUtenso
                                          (issued.y >> i) & 1u))
                         atomicOr(&g_status_word, kStatusDrainTimeout);
         }
-        if (warp == 9 && elect_one()) {   // (the same lane again)
+        if (warp == 17 && elect_one()) {   // (the same lane again)
             umma_commit(bars.drain());
             if (!mbar_wait_drain(bars.drain(), 0)) atomicOr(&g_status_word, kStatusDrainTimeout);
         }
@@ -1331,29 +1308,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // the prologue's sums, in the statistics' place
     long long *warp_sums = reinterpret_cast<long long *>(tree_stats<D>(smem));
 
-    if (warp == 8 && lane == 0) {
+    if (warp == 16 && lane == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
             mbar_init(bars.kv_full(s), 1);
-            mbar_init(bars.kv_empty(s), 2);   // the MMAs' completion and warp 10
+            mbar_init(bars.kv_empty(s), 2);   // the MMAs' completion and warp 18
             mbar_init(bars.v_fixed(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bars.q_full(s), 1);
             mbar_init(bars.q_empty(s), 1);
             mbar_init(bars.s_full(s), 1);
-            mbar_init(bars.p_ready(s), 4);
-            mbar_init(bars.p_half(s), 4);
+            mbar_init(bars.p_ready(s), 8);
             mbar_init(bars.o_full(s), 1);
-        }
-        for (int w = 0; w < 4; ++w) {
-            mbar_init(bars.st_ready(w), 2);
-            mbar_init(bars.o_done(w), 2);
         }
         for (int i = 0; i < kTreeEntries; ++i) {
             mbar_init(bars.e_full(i), 1);
-            mbar_init(bars.e_empty(i), 9);    // the softmax warps and warp 10
+            mbar_init(bars.e_empty(i), 17);   // the softmax warps and warp 18
         }
-        mbar_init(bars.both_ready(), 8);
+        mbar_init(bars.both_ready(), 16);
+        mbar_init(bars.o_done(), 16);
         mbar_init(bars.drain(), 1);
         *tree_abort<D>(smem) = 0;
         start->units = 0;
@@ -1363,7 +1336,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(smem_u32(tmem_holder), 512);
         tmem_relinquish();
         tc_fence_before();
@@ -1457,7 +1430,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tree_block<D, true>(tmQn, tmK, tmV, a, blk, *start, [&](int r) { return on_line(r, true); });
     else
         tree_block<D, false>(tmQ, tmK, tmV, a, blk, *start, [&](int r) { return on_line(r, false); });
-    if (warp == 9) {
+    if (warp == 17) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(blk.tmem, 512);
