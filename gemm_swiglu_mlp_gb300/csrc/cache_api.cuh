@@ -62,9 +62,6 @@ int launch_overlapped(void (*kernel)(Args), dim3 grid, unsigned threads, size_t 
     return SWIGLU_OK;
 }
 
-// Tiles a block takes at least.
-constexpr int kTreeMinUnits = 1;
-
 // Workspace of one attention call: which items go on in another block, and
 // two partial results a block (of the item it takes over and of the one it
 // leaves).
@@ -438,8 +435,10 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     a.geom.kv_heads = static_cast<int>(kv_heads);
     a.geom.group = static_cast<int>(group);
     a.geom.tpt = kTreeTile / static_cast<int>(group);
+    a.geom.recip = tree_recip(a.geom.tpt);
     a.geom.causal = mask == nullptr;
     a.geom.max_rows = static_cast<int>(max_pages << shape.page_shift);
+    if (!tree_fits(a.geom)) return SWIGLU_ERR_UNSUPPORTED;
     a.table = block_table;
     a.ctx_lens = ctx_lens;
     a.query_start = query_start;
@@ -457,7 +456,6 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     a.page_shift = shape.page_shift;
     a.mask_words = static_cast<int>(mask_words);
     a.part_rows = ws.rows;
-    a.min_units = kTreeMinUnits;
     const uint64_t pages_heads = static_cast<uint64_t>(num_pages) * static_cast<uint64_t>(kv_heads);
     CUtensorMap tmQ, tmQn, tmK, tmV;
     const uint64_t D = static_cast<uint64_t>(head_dim);

@@ -497,6 +497,10 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
+// The same with one column.
+__device__ __forceinline__ void tmem_ld_32x32b_x1(uint32_t taddr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
 // The same with 8 consecutive columns.
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -569,6 +573,9 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void reg_fence4(uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+    asm volatile("" : "+r"(a), "+r"(b), "+r"(c), "+r"(d) : : "memory");
+}
 __device__ __forceinline__ void reg_fence8(uint32_t (&r)[8]) {
     asm volatile(""
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),

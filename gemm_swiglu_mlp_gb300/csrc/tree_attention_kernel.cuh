@@ -45,6 +45,13 @@
 // other; how an entry gives both groups work is said at TreeEntry.
 // Every wait is bounded (sm103_ptx.cuh); a group's barriers are reached by all
 // of its warps whatever their waits said.
+//
+// Five roles run different code at once, and the SM's instruction cache holds
+// some 32 KB: the roles read what they follow from shared memory instead of
+// keeping copies, have one call site for each kind of step, and leave loops
+// rolled where a step is long anyway (with everything inlined and unrolled,
+// 290 KB, a quarter of the fetches missed and warps waited longer for
+// instructions than for scores).
 #pragma once
 
 #include "epilogue.cuh"
@@ -67,7 +74,6 @@ struct TreeAttnArgs {
     float scale_log2;                  // scale * log2(e)
     int q_heads, num_pages, page_shift, mask_words;
     int part_rows;                     // rows of one partial result: 128 or 256
-    int min_units;                     // tiles a block, at least
 };
 
 constexpr int kTreeEntries = 4;   // entries described ahead of their results
@@ -101,7 +107,7 @@ struct TreeShared {
     static constexpr int OFF_STATS = BASE;                  // float2 [2][128]
     static constexpr int OFF_ENTRY = OFF_STATS + 2 * 128 * 8;
     static constexpr int OFF_BAR = OFF_ENTRY + kTreeEntries * static_cast<int>(sizeof(TreeEntry));
-    static constexpr int STAGES = 11;                       // the most a form has
+    static constexpr int STAGES = D == 128 ? 6 : 11;        // the most a form has
     // ring: full, empty, V fixed; two Q buffers: full, empty; a group: scores,
     // weights, result; entries: full, empty; both groups: statistics, results
     // read; drain
@@ -256,11 +262,27 @@ __device__ __noinline__ void tree_add_nonfinite(T *result, int cols, const TreeS
     }
 }
 
-// A bounded wait by a whole warp: every lane gets the same answer, so that no
-// lane is left alone at a later warp-wide instruction.
+// mbar_wait with its loop out of line: the first try, which the hardware may
+// suspend for a while, mostly succeeds.
+__device__ __noinline__ bool tree_wait_on(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+    return mbar_wait(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity,
+                                          const volatile int *abort_flag) {
+    return mbar_try_wait(bar, parity) || tree_wait_on(bar, parity, abort_flag);
+}
+// The same by a whole warp: every lane gets the same answer, so that no lane
+// is left alone at a later warp-wide instruction.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
                                           const volatile int *abort_flag) {
-    return __all_sync(~0u, mbar_wait(bar, parity, abort_flag));
+    return __all_sync(~0u, tree_wait(bar, parity, abort_flag));
+}
+// This thread gave up: says so, and tells the others to leave.
+__device__ __noinline__ void tree_give_up(volatile int *abort_flag, unsigned int status) {
+    if (!*abort_flag) {
+        atomicOr(&g_status_word, status);
+        *abort_flag = 1;
+    }
 }
 
 // Barriers over the eight warps of softmax group s (named barriers 1 and 2).
@@ -280,40 +302,19 @@ __device__ __forceinline__ bool group_any(int s, bool v) {
     return r != 0;
 }
 
-// Sum over the block of one number a thread: before this thread, and in all.
-struct TreeScan {
-    long long before, total;
-};
-__device__ __forceinline__ TreeScan tree_block_scan(long long mine, long long *warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long in = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(~0u, in, d);
-        if (lane >= d) in += x;
-    }
-    if (lane == 31) warp_sums[warp] = in;
-    __syncthreads();
-    TreeScan s{in - mine, 0};
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
-        if (w < warp) s.before += warp_sums[w];
-        s.total += warp_sums[w];
-    }
-    return s;
-}
-
-// What a role follows: the block's entries, step by step, and the ring's stages
-// in the order that the producer, the MMA issuer and the V warp all keep: per
-// step, for each group in turn, the V tile of this step and the K tile of the
-// next.
+// What the producer, the MMA issuer and the V warp follow: the entries step by
+// step, and the ring's stages in the order that all three keep: per step, for
+// each group in turn, the V tile of this step and the K tile of the next. The
+// step before the first has no V tiles.
 template <int D, bool NARROW>
 struct TreeCursor {
     using C = TreeCfg<D, NARROW>;
-    const TreeEntry *entries;
     TreeBars<D> bars;
+    const TreeEntry *entries;
     const volatile int *abort_flag;
-    TreeEntry cur, nxt;
-    int step, nstep, seq, stage;
+    const TreeEntry *cur, *nxt;   // entries of this step (null before the first) and the next
+    int step, nstep, seq;         // the steps' numbers; entry nxt's
+    int stage;
     uint32_t phase;
 
     __device__ __forceinline__ void advance() {
@@ -322,32 +323,28 @@ struct TreeCursor {
             phase ^= 1u;
         }
     }
-    __device__ __forceinline__ bool fetch(TreeEntry &e) {   // entry `seq`, once it is described
+    // Once entry `seq` is described, the next step is its first.
+    __device__ __forceinline__ bool fetch() {
         const int i = seq % kTreeEntries;
-        const bool got = mbar_wait(bars.e_full(i), (seq / kTreeEntries) & 1, abort_flag);
-        e = entries[i];
-        return got;
+        nxt = entries + i;
+        nstep = 0;
+        return tree_wait(bars.e_full(i), (seq / kTreeEntries) & 1, abort_flag);
     }
     __device__ __forceinline__ bool start() {
+        cur = nullptr;
         step = seq = stage = 0;
         phase = 0;
-        return fetch(cur);
+        return fetch();
     }
-    __device__ __forceinline__ bool follow() {   // nxt, nstep: the step after (cur, step)
-        nxt = cur;
-        nstep = step + 1;
-        if (nstep < cur.steps) return true;
-        nstep = 0;
-        ++seq;
-        return fetch(nxt);
-    }
-    __device__ __forceinline__ void move() {
+    // To the next step, giving back the entry that is left.
+    __device__ __forceinline__ bool move(bool arrive) {
+        if (cur && cur != nxt && arrive) mbar_arrive(bars.e_empty((seq - 1) % kTreeEntries));
         cur = nxt;
         step = nstep;
-    }
-    // group s has a tile of its own in a step
-    __device__ __forceinline__ static bool own_kv(const TreeEntry &e, int st, int s) {
-        return e.part[s].active(st) && (s == 0 || e.two_kv());
+        nstep = step + 1;
+        if (nstep < cur->steps) return true;
+        ++seq;
+        return fetch();
     }
 };
 
@@ -361,80 +358,72 @@ __device__ __forceinline__ uint2 tree_produce(const CUtensorMap &tmQ, const CUte
     using C = TreeCfg<D, NARROW>;
     const TreeGeom &g = a.geom;
     const TreeBars<D> bars{smem_u32(blk.smem)};
-    const uint32_t sbase = bars.base;
     const int lane = threadIdx.x & 31;
     volatile int *abort_flag = tree_abort<D>(blk.smem);
-    TreeCursor<D, NARROW> k{tree_entries<D>(blk.smem), bars, abort_flag};
-    bool ok = true;
+    TreeCursor<D, NARROW> k{bars, tree_entries<D>(blk.smem), abort_flag};
     uint32_t issued = 0, parity = 0;   // bits: ring stages, then the two Q tiles
     int qb = 0;
     uint32_t qphase = 0;
     const int pages = kTreeTile >> a.page_shift;   // pages a tile, <= 8
-    auto load_tile = [&](const CUtensorMap &tm, const TreePart &x, int tile) {
-        const int left = x.len - tile * kTreeTile;   // positions of the tile, > 0
-        const int count = tree_min(pages, (left + (1 << a.page_shift) - 1) >> a.page_shift);
-        int row = 0;
-        if (lane < count) {
-            const int page = a.table[x.r * a.max_pages +
-                                     static_cast<long long>(tile) * pages + lane];
-            // outside the cache: a box past its end, filled with zeros
-            row = page >= 0 && page < a.num_pages ? page * g.kv_heads + x.h
-                                                  : a.num_pages * g.kv_heads;
-        }
-        if (!warp_wait(bars.kv_empty(k.stage), k.phase ^ 1u, abort_flag)) return false;
-        const uint32_t bytes = static_cast<uint32_t>(count) * kRowBytes * C::HALVES
-                               << a.page_shift;
-        if (lane == 0) mbar_arrive_expect_tx(bars.kv_full(k.stage), bytes);
-        __syncwarp();
-        const uint32_t dst =
-            sbase + C::OFF_KV + k.stage * C::TILE +
-            (static_cast<uint32_t>(lane) * C::HALVES * kRowBytes << a.page_shift);
-        if (lane < count) tma_load_5d(dst, &tm, bars.kv_full(k.stage), 0, 0, 0, 0, row);
-        issued |= 1u << k.stage;
-        parity = (parity & ~(1u << k.stage)) | (k.phase << k.stage);
-        k.advance();
-        return true;
-    };
-    auto load_q = [&](const TreePart &x) {
-        if (!warp_wait(bars.q_empty(qb), ((qphase >> qb) & 1u) ^ 1u, abort_flag)) return false;
-        // a box of the row tile (rows past its tokens are not used)
-        const int toks = (NARROW ? kTreeNarrow : kTreeTile) / g.group;
-        if (lane == 0)
-            mbar_arrive_expect_tx(bars.q_full(qb), static_cast<uint32_t>(toks) * g.group *
-                                                  kRowBytes * C::HALVES);
-        __syncwarp();
-        if (lane < C::HALVES)
-            tma_load_3d(sbase + C::OFF_Q + qb * C::QBUF + lane * C::Q_HALF, &tmQ,
-                        bars.q_full(qb), 64 * lane, x.h * g.group, x.tok);
-        const int bit = C::STAGES + qb;
-        issued |= 1u << bit;
-        parity = (parity & ~(1u << bit)) | (((qphase >> qb) & 1u) << bit);
-        qphase ^= 1u << qb;
-        qb ^= 1;
-        return true;
-    };
-    // group s's K tile of a k.step (Q too at an entry's first)
-    auto load_k = [&](const TreeEntry &e, int st, int s) {
-        if (st == 0 && e.steps > 0 && (s == 0 || e.two_q()) && !load_q(e.part[s]))
-            return false;
-        return !k.own_kv(e, st, s) || load_tile(tmK, e.part[s], e.part[s].tile(st));
-    };
-    ok = __all_sync(~0u, k.start());
-    if (ok && k.cur.steps) ok = load_k(k.cur, 0, 0) && load_k(k.cur, 0, 1);
-    while (ok && k.cur.steps) {
-        ok = __all_sync(~0u, k.follow());
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
+    bool ok = __all_sync(~0u, k.start());
+    while (ok && (k.cur || k.nxt->steps)) {
+#pragma unroll 1
+        for (int op = 0; op < 4; ++op) {   // V of group 0, K of group 0, V and K of group 1
+            const bool is_k = op & 1;
+            const int s = op >> 1, step = is_k ? k.nstep : k.step;
+            const TreeEntry *e = is_k ? k.nxt : k.cur;
+            if (!e || step >= e->steps) continue;
+            const TreePart &x = e->part[s];
+            if (is_k && step == 0 && (s == 0 || e->two_q())) {
+                // the row tile's queries (rows past its tokens are not used)
+                ok = warp_wait(bars.q_empty(qb), ((qphase >> qb) & 1u) ^ 1u, abort_flag);
+                if (!ok) break;
+                const int toks = (NARROW ? kTreeNarrow : kTreeTile) / g.group;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bars.q_full(qb), static_cast<uint32_t>(toks) * g.group *
+                                                               kRowBytes * C::HALVES);
+                __syncwarp();
+                if (lane < C::HALVES)
+                    tma_load_3d(bars.base + C::OFF_Q + qb * C::QBUF + lane * C::Q_HALF, &tmQ,
+                                bars.q_full(qb), 64 * lane, x.h * g.group, x.tok);
+                const int bit = C::STAGES + qb;
+                issued |= 1u << bit;
+                parity = (parity & ~(1u << bit)) | (((qphase >> qb) & 1u) << bit);
+                qphase ^= 1u << qb;
+                qb ^= 1;
+            }
+            if (!e->own_kv(step, s)) continue;
+            const int tile = x.tile(step);
+            // the tile's pages up to the item's end
+            const int count = tree_min(
+                pages, (x.len - tile * kTreeTile + (1 << a.page_shift) - 1) >> a.page_shift);
+            int row = 0;
+            if (lane < count) {
+                const int page = a.table[x.r * a.max_pages +
+                                         static_cast<long long>(tile) * pages + lane];
+                // outside the cache: a box past its end, filled with zeros
+                row = page >= 0 && page < a.num_pages ? page * g.kv_heads + x.h
+                                                      : a.num_pages * g.kv_heads;
+            }
+            ok = warp_wait(bars.kv_empty(k.stage), k.phase ^ 1u, abort_flag);
             if (!ok) break;
-            if (k.own_kv(k.cur, k.step, s)) ok = load_tile(tmV, k.cur.part[s], k.cur.part[s].tile(k.step));
-            if (k.nxt.steps) ok = ok && load_k(k.nxt, k.nstep, s);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bars.kv_full(k.stage), static_cast<uint32_t>(count) *
+                                                                 kRowBytes * C::HALVES
+                                                                 << a.page_shift);
+            __syncwarp();
+            if (lane < count)
+                tma_load_5d(bars.base + C::OFF_KV + k.stage * C::TILE +
+                                (static_cast<uint32_t>(lane) * C::HALVES * kRowBytes << a.page_shift),
+                            is_k ? &tmK : &tmV, bars.kv_full(k.stage), 0, 0, 0, 0, row);
+            issued |= 1u << k.stage;
+            parity = (parity & ~(1u << k.stage)) | (k.phase << k.stage);
+            k.advance();
         }
-        k.move();
+        if (ok && k.nxt->steps == 0) break;
+        if (ok) ok = __all_sync(~0u, k.move(lane == 0));
     }
-    if (!ok && lane == 0 && !*abort_flag) {
-        atomicOr(&g_status_word, kStatusProducerTimeout);
-        *abort_flag = 1;
-    }
+    if (!ok && lane == 0) tree_give_up(abort_flag, kStatusProducerTimeout);
     return make_uint2(issued, parity);
 }
 
@@ -443,10 +432,8 @@ template <int D, bool NARROW>
 __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
     using C = TreeCfg<D, NARROW>;
     const TreeBars<D> bars{smem_u32(blk.smem)};
-    const uint32_t sbase = bars.base;
     volatile int *abort_flag = tree_abort<D>(blk.smem);
-    TreeCursor<D, NARROW> k{tree_entries<D>(blk.smem), bars, abort_flag};
-    bool ok = true;
+    TreeCursor<D, NARROW> k{bars, tree_entries<D>(blk.smem), abort_flag};
     // the scores: 128 rows x 128 positions, or 128 positions x 32 rows
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, NARROW ? kTreeNarrow : kTreeTile);
     // the result: 128 rows x D, V as it lies; or D x 32 rows, both as they lie
@@ -456,99 +443,102 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
     // narrow: the weights' sums, as a product with a block of ones, so that they
     // need no registers during the tiles and no exchange between threads
     constexpr uint32_t idesc_l = idesc_bf16_f32(128, kTreeNarrow) | kIdescBMnMajor;
-    // the first Q buffer of entry k.cur, and of k.nxt
-    int qb = 0, nqb = 0, kstage = 0, vstage = 0;
+    // the next entry's first Q tile, the stages of the K and V tiles in use
+    int qb = 0, kstage = 0, vstage = 0;
     uint32_t qphase = 0, pphase = 0, fphase = 0;
-    auto qbuf = [&](const TreeEntry &e, int b, int s) { return e.two_q() ? b ^ s : b; };
-    // scores of group s for a k.step
-    auto scores = [&](const TreeEntry &e, int st, int s, int b) {
-        const TreePart &x = e.part[s];
-        if (!x.active(st)) return true;
-        const int buf = qbuf(e, b, s);
-        if (st == 0 && (s == 0 || e.two_q())) {
-            if (!mbar_wait(bars.q_full(buf), (qphase >> buf) & 1u, abort_flag)) return false;
-            qphase ^= 1u << buf;
-        }
-        if (s == 0 || e.two_kv()) {
-            if (!mbar_wait(bars.kv_full(k.stage), k.phase, abort_flag)) return false;
-            kstage = k.stage;
-            k.advance();
-        }
-        tc_fence_after();
-        const uint32_t qa = sbase + C::OFF_Q + buf * C::QBUF;
-        const uint64_t kd =
-            smem_desc(sbase + C::OFF_KV + kstage * C::TILE, 16, C::GROUP);
-        const uint64_t qd = smem_desc(qa, 16, 1024);
+    bool ok = k.start();
+    while (ok && (k.cur || k.nxt->steps)) {
+#pragma unroll 1
+        for (int op = 0; op < 4; ++op) {
+            const bool is_k = op & 1;
+            const int s = op >> 1, step = is_k ? k.nstep : k.step;
+            const TreeEntry *e = is_k ? k.nxt : k.cur;
+            if (!e || step >= e->steps) continue;
+            const TreePart &x = e->part[s];
+            if (!x.active(step)) continue;
+            const int tile = x.tile(step);
+            const bool own = e->own_kv(step, s);
+            const bool last_use = s == 1 || e->kind != kTreePair;   // of the K or V tile
+            if (is_k) {
+                const int buf = e->two_q() ? qb ^ s : qb;
+                if (step == 0 && (s == 0 || e->two_q())) {
+                    ok = tree_wait(bars.q_full(buf), (qphase >> buf) & 1u, abort_flag);
+                    if (!ok) break;
+                    qphase ^= 1u << buf;
+                }
+                if (own) {
+                    ok = tree_wait(bars.kv_full(k.stage), k.phase, abort_flag);
+                    if (!ok) break;
+                    kstage = k.stage;
+                    k.advance();
+                }
+                tc_fence_after();
+                const uint64_t kd =
+                    smem_desc(bars.base + C::OFF_KV + kstage * C::TILE, 16, C::GROUP);
+                const uint64_t qd = smem_desc(bars.base + C::OFF_Q + buf * C::QBUF, 16, 1024);
+                const uint32_t acc = blk.tmem + 128 * s;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint64_t ko = kd + (i >> 2) * (1024 >> 4) + 2u * (i & 3);
-            const uint64_t qo = qd + (i >> 2) * (C::Q_HALF >> 4) + 2u * (i & 3);
-            umma_bf16(blk.tmem + 128 * s, NARROW ? ko : qo, NARROW ? qo : ko, idesc_s,
-                      i != 0);
-        }
-        umma_commit(bars.s_full(s));
-        if (s == 1 || e.two_kv()) umma_commit(bars.kv_empty(kstage));
-        // the last scores that need this Q tile
-        if (x.tile(st) + 1 == x.end) umma_commit(bars.q_empty(buf));
-        return true;
-    };
-    ok = k.start();
-    if (ok && k.cur.steps) ok = scores(k.cur, 0, 0, qb) && scores(k.cur, 0, 1, qb);
-    while (ok && k.cur.steps) {
-        ok = k.follow();
-        nqb = k.nstep == 0 && !k.cur.two_q() ? qb ^ 1 : qb;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (!ok) break;
-            const TreePart &x = k.cur.part[s];
-            if (x.active(k.step)) {
-                if (s == 0 || k.cur.two_kv()) {
-                    ok = mbar_wait(bars.kv_full(k.stage), k.phase, abort_flag);
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t ko = kd + (i >> 2) * (1024 >> 4) + 2u * (i & 3);
+                    const uint64_t qo = qd + (i >> 2) * (C::Q_HALF >> 4) + 2u * (i & 3);
+                    umma_bf16(acc, NARROW ? ko : qo, NARROW ? qo : ko, idesc_s, i != 0);
+                }
+                umma_commit(bars.s_full(s));
+                if (last_use) umma_commit(bars.kv_empty(kstage));
+                // the last scores that need this Q tile
+                if (tile + 1 == x.end) {
+                    umma_commit(bars.q_empty(buf));
+                    if (!e->two_q()) qb ^= 1;
+                }
+            } else {
+                if (own) {
+                    ok = tree_wait(bars.kv_full(k.stage), k.phase, abort_flag);
+                    if (!ok) break;
                     vstage = k.stage;
                     k.advance();
-                    if (ok && x.edge(x.tile(k.step))) {
-                        ok = mbar_wait(bars.v_fixed(vstage), (fphase >> vstage) & 1u,
-                                       abort_flag);
+                    if (x.edge(tile)) {
+                        ok = tree_wait(bars.v_fixed(vstage), (fphase >> vstage) & 1u, abort_flag);
+                        if (!ok) break;
                         fphase ^= 1u << vstage;
                     }
                 }
-                const uint64_t vd = smem_desc(sbase + C::OFF_KV + vstage * C::TILE,
+                ok = tree_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
+                if (!ok) break;
+                pphase ^= 1u << s;
+                tc_fence_after();
+                // positions of the tile, in 16s (the rest has no weight)
+                const int count = tree_min(8, (x.len - tile * kTreeTile + 15) >> 4);
+                const uint64_t vd = smem_desc(bars.base + C::OFF_KV + vstage * C::TILE,
                                               D == 128 ? 1024 : 0, C::GROUP);
                 const uint32_t acc = blk.tmem + TreeShared<D>::TMEM_O + D * s;
                 constexpr uint32_t kstep = 2 * C::GROUP >> 4;   // 16 positions of V
-                ok = ok && mbar_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
+                const uint32_t more = step != 0;
                 if constexpr (NARROW) {
                     const uint64_t wd =
-                        smem_desc(sbase + C::OFF_W + s * C::W_BYTES, 16, 512, 4);
+                        smem_desc(bars.base + C::OFF_W + s * C::W_BYTES, 16, 512, 4);
 #pragma unroll
-                    for (int i = 0; i < kTreeTile / 16; ++i)
-                        umma_bf16(acc, vd + kstep * i, wd + 64u * i, idesc_o,
-                                  k.step != 0 || i != 0);
-#pragma unroll
-                    for (int i = 0; i < kTreeTile / 16; ++i)
+                    for (int i = 0; i < kTreeTile / 16; ++i) {
+                        if (i >= count) break;
+                        umma_bf16(acc, vd + kstep * i, wd + 64u * i, idesc_o, more || i != 0);
                         umma_bf16_ts(acc + 32, blk.tmem + TreeShared<D>::TMEM_ONES, wd + 64u * i,
-                                     idesc_l, k.step != 0 || i != 0);
+                                     idesc_l, more || i != 0);
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kTreeTile / 16; ++i)
+                    for (int i = 0; i < kTreeTile / 16; ++i) {
+                        if (i >= count) break;
                         umma_bf16_ts(acc, blk.tmem + 128 * s + 64 * (i >> 2) + 8 * (i & 3),
-                                     vd + kstep * i, idesc_o, k.step != 0 || i != 0);
+                                     vd + kstep * i, idesc_o, more || i != 0);
+                    }
                 }
-                pphase ^= 1u << s;
-                if (s == 1 || k.cur.two_kv()) umma_commit(bars.kv_empty(vstage));
-                if (x.last(k.step)) umma_commit(bars.o_full(s));
+                if (last_use) umma_commit(bars.kv_empty(vstage));
+                if (tile + x.stride >= x.end) umma_commit(bars.o_full(s));
             }
-            if (k.nxt.steps) ok = scores(k.nxt, k.nstep, s, nqb);
         }
-        k.move();
-        qb = nqb;
+        if (ok && k.nxt->steps == 0) break;
+        if (ok) ok = k.move(true);
     }
-    if (!ok && !*abort_flag) {
-        atomicOr(&g_status_word, kStatusMmaTimeout);
-        *abort_flag = 1;
-    }
+    if (!ok) tree_give_up(abort_flag, kStatusMmaTimeout);
 }
 
 // ---- V rows of edge tiles. Every stage is waited for and given back in ring
@@ -561,89 +551,70 @@ __device__ __forceinline__ void tree_mend_v(const TreeBlock &blk) {
     const TreeBars<D> bars{smem_u32(blk.smem)};
     const int lane = threadIdx.x & 31;
     volatile int *abort_flag = tree_abort<D>(blk.smem);
-    volatile int *flags = tree_flags<D>(blk.smem);
-    TreeCursor<D, NARROW> k{tree_entries<D>(blk.smem), bars, abort_flag};
-    bool ok = true;
-    auto pass = [&] {
-        const bool full = warp_wait(bars.kv_full(k.stage), k.phase, abort_flag);
-        if (lane == 0) mbar_arrive(bars.kv_empty(k.stage));
-        k.advance();
-        return full;
-    };
-    ok = __all_sync(~0u, k.start());
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-        if (ok && k.cur.steps && k.own_kv(k.cur, 0, s)) ok = pass();
-    while (ok && k.cur.steps) {
-        const int slot = k.seq % kTreeEntries;
-        ok = __all_sync(~0u, k.follow());
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
+    TreeCursor<D, NARROW> k{bars, tree_entries<D>(blk.smem), abort_flag};
+    bool ok = __all_sync(~0u, k.start());
+    while (ok && (k.cur || k.nxt->steps)) {
+#pragma unroll 1
+        for (int op = 0; op < 4; ++op) {
+            const bool is_k = op & 1;
+            const int s = op >> 1, step = is_k ? k.nstep : k.step;
+            const TreeEntry *e = is_k ? k.nxt : k.cur;
+            if (!e || step >= e->steps || !e->own_kv(step, s)) continue;
+            ok = warp_wait(bars.kv_full(k.stage), k.phase, abort_flag);
             if (!ok) break;
-            if (k.own_kv(k.cur, k.step, s)) {
-                const int at = k.stage;
-                ok = warp_wait(bars.kv_full(at), k.phase, abort_flag);
-                if (!ok) break;
-                const TreePart &x = k.cur.part[s];
-                if (x.edge(x.tile(k.step))) {
-                    const int x0 = x.tile(k.step) * kTreeTile;
-                    // rows [first, end) hold new tokens, [end, 128) nothing;
-                    // a row's 16-byte chunks are permuted within its 128 bytes
-                    const int end = tree_min(x.len - x0, kTreeTile);
-                    const int first = tree_min(tree_max(x.ctx - x0, 0), end);
-                    bool bad = false;
-                    // 16-byte chunk i of the rows' halves, row by row
-                    uint8_t *base = blk.smem + C::OFF_KV + at * C::TILE;
-                    constexpr int chunks = C::HALVES * 8;   // a row
-                    auto chunk = [&](int i) {
-                        const int r = i / chunks, k = i % chunks;
-                        return reinterpret_cast<uint4 *>(
-                            base + (r >> 3) * C::GROUP + (k >> 3) * 1024 +
-                            (r & 7) * kRowBytes + (k & 7) * 16);
-                    };
-                    for (int i = end * chunks + lane; i < kTreeTile * chunks; i += 32)
-                        *chunk(i) = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-                    for (int i = first * chunks + lane; i < end * chunks; i += 32) {
-                        uint4 *at16 = chunk(i);
-                        const uint4 v = *at16;
-                        uint32_t any = 0;   // exponent all ones: carry
-                        any |= (v.x & 0x7F807F80u) + 0x00800080u;
-                        any |= (v.y & 0x7F807F80u) + 0x00800080u;
-                        any |= (v.z & 0x7F807F80u) + 0x00800080u;
-                        any |= (v.w & 0x7F807F80u) + 0x00800080u;
-                        if (any & 0x80008000u) {
-                            uint32_t *e = reinterpret_cast<uint32_t *>(at16);
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t z = e[k];
-                                if ((z & 0x7F80u) == 0x7F80u) z &= 0xFFFF0000u;
-                                if ((z & 0x7F800000u) == 0x7F800000u) z &= 0xFFFFu;
-                                e[k] = z;
-                            }
-                            bad = true;
-                        }
+            const TreePart &x = e->part[s];
+            const int tile = x.tile(step);
+            if (!is_k && x.edge(tile)) {
+                // rows [first, end) hold new tokens, [end, 128) nothing (of
+                // which the product reads those up to a multiple of 16); a
+                // row's 16-byte chunks are permuted within its 128 bytes
+                const int end = tree_min(x.len - tile * kTreeTile, kTreeTile);
+                const int first = tree_min(tree_max(x.ctx - tile * kTreeTile, 0), end);
+                const int stop = (end + 15) & ~15;
+                uint8_t *base = blk.smem + C::OFF_KV + k.stage * C::TILE;
+                constexpr int chunks = C::HALVES * 8;   // a row
+                bool bad = false;
+#pragma unroll 1
+                for (int i = first * chunks + lane; i < stop * chunks; i += 32) {
+                    const int r = i / chunks, c = i % chunks;
+                    uint4 *at = reinterpret_cast<uint4 *>(base + (r >> 3) * C::GROUP +
+                                                          (c >> 3) * 1024 + (r & 7) * kRowBytes +
+                                                          (c & 7) * 16);
+                    if (r >= end) {
+                        *at = make_uint4(0, 0, 0, 0);
+                        continue;
                     }
-                    if (bad) {
-                        flags[2 * slot + s] = 1;
-                        if (!k.cur.two_kv()) flags[2 * slot + 1] = 1;
+                    const uint4 v = *at;
+                    // exponent all ones: carry
+                    const uint32_t any = ((v.x & 0x7F807F80u) + 0x00800080u) |
+                                         ((v.y & 0x7F807F80u) + 0x00800080u) |
+                                         ((v.z & 0x7F807F80u) + 0x00800080u) |
+                                         ((v.w & 0x7F807F80u) + 0x00800080u);
+                    if (any & 0x80008000u) {
+                        bad = true;
+                        uint16_t *h = reinterpret_cast<uint16_t *>(at);
+#pragma unroll 1
+                        for (int j = 0; j < 8; ++j)
+                            if ((h[j] & 0x7F80u) == 0x7F80u) h[j] = 0;
                     }
-                    __threadfence_block();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.v_fixed(at));
                 }
-                if (lane == 0) mbar_arrive(bars.kv_empty(at));
-                k.advance();
+                if (bad) {
+                    volatile int *flags = tree_flags<D>(blk.smem) + 2 * (e - k.entries);
+                    flags[s] = 1;
+                    if (e->kind == kTreePair) flags[1] = 1;
+                }
+                __threadfence_block();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.v_fixed(k.stage));
             }
-            if (k.nxt.steps && k.own_kv(k.nxt, k.nstep, s)) ok = ok && pass();
+            if (lane == 0) mbar_arrive(bars.kv_empty(k.stage));
+            k.advance();
         }
-        if (k.nstep == 0 && lane == 0) mbar_arrive(bars.e_empty(slot));
-        k.move();
+        if (ok && k.nxt->steps == 0) break;
+        if (ok) ok = __all_sync(~0u, k.move(lane == 0));
     }
-    if (!ok && lane == 0 && !*abort_flag) {
-        atomicOr(&g_status_word, kStatusEpilogueTimeout);
-        *abort_flag = 1;
-    }
+    if (!ok && lane == 0) tree_give_up(abort_flag, kStatusEpilogueTimeout);
 }
 
 // ---- entries, ahead of their use: one thread
@@ -656,35 +627,31 @@ __device__ __forceinline__ void tree_describe(const TreeAttnArgs &a, const TreeB
     volatile int *flags = tree_flags<D>(blk.smem);
     TreeEntry *entries = tree_entries<D>(blk.smem);
     TreeWalk w{};
-    w.begin(g, start, load);
+    if (start.units > 0) w.begin(g, start);
     int4 chain = make_int4(0, 0, 0, 0);
     bool ok = true;
     int seq = 0;
     for (bool more = true; more; ++seq) {
         const int i = seq % kTreeEntries;
-        const TreeEntry e = w.entry(g, load);
-        more = e.steps > 0;
-        ok = mbar_wait(bars.e_empty(i), ((seq / kTreeEntries) & 1) ^ 1, abort_flag);
+        ok = tree_wait(bars.e_empty(i), ((seq / kTreeEntries) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        entries[i] = e;
+        TreeEntry *e = entries + i;
+        w.entry(g, load, e);
         flags[2 * i] = flags[2 * i + 1] = 0;
-        mbar_arrive(bars.e_full(i));
+        more = e->steps > 0;
         // an item that begins here and goes on in the next blocks
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const TreePart &x = e.part[s];
-            if (!more || (x.flags & (kPartWhole | kPartBegins | kPartSecond)) != kPartBegins) continue;
+        for (int s = 0; s < 2 && more; ++s) {
+            const TreePart &x = e->part[s];
+            if ((x.flags & (kPartWhole | kPartBegins | kPartSecond)) != kPartBegins) continue;
             const int rest = (x.len + kTreeTile - 1) / kTreeTile - x.end;
-            const long long last = tree_block_begin(blk.cut, blk.index + 1) + rest - 1;
+            const int last = tree_block_begin(blk.cut, blk.index + 1) + rest - 1;
             chain = make_int4(blk.base + tree_block_of(blk.cut, last), x.tok, x.h,
-                              x.ntok + (e.kind == kTreePair ? e.part[1].ntok : 0));
+                              x.ntok + (e->kind == kTreePair ? e->part[1].ntok : 0));
         }
+        mbar_arrive(bars.e_full(i));
     }
     a.chains[blockIdx.x] = chain;
-    if (!ok && !*abort_flag) {
-        atomicOr(&g_status_word, kStatusProducerTimeout);
-        *abort_flag = 1;
-    }
+    if (!ok) tree_give_up(abort_flag, kStatusProducerTimeout);
 }
 
 // Where a softmax warp is in the barriers' phases.
@@ -745,10 +712,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
     const float sc = a.scale_log2;
     bool good = true;
     auto give_up = [&] {
-        if (lane == 0 && !*abort_flag) {
-            atomicOr(&g_status_word, kStatusEpilogueTimeout);
-            *abort_flag = 1;
-        }
+        if (lane == 0) tree_give_up(abort_flag, kStatusEpilogueTimeout);
         good = false;
     };
     if (!tree_results_read<D>(bars, ph, abort_flag)) give_up();
@@ -893,52 +857,39 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
         static_cast<long long>(2 * c + ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows;
     const float *m0 = tree_stats<D>(blk.smem) + kMax, *m1 = m0 + 256;
     const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
-    // the halves of a group, in a split all four, take eights of rows in turn;
-    // with up to eight rows the rows
+    // the halves of a group, in a split all four, take the rows in turn
     const int turns = split ? 4 : 2, turn = split ? 2 * s + half : half;
-    const bool by_row = rows <= 8;
     const long long first_row = static_cast<long long>(x.tok) * a.q_heads + x.h * g.group;
 #pragma unroll 1
-    for (int n0 = by_row ? 0 : 8 * turn; n0 < rows; n0 += by_row ? 8 : 8 * turns) {
-        uint32_t o[8], l[8], y[8], z[8];
-        tmem_ld_32x32b_x8((split ? t0 : to) + n0, o);
-        tmem_ld_32x32b_x8((split ? t0 : to) + 32 + n0, l);
+    for (int r = turn; r < rows; r += turns) {
+        uint32_t o, l, y = 0, z = 0;
+        tmem_ld_32x32b_x1((split ? t0 : to) + r, o);
+        tmem_ld_32x32b_x1((split ? t0 : to) + 32 + r, l);
         if (split && used1) {
-            tmem_ld_32x32b_x8(t1 + n0, y);
-            tmem_ld_32x32b_x8(t1 + 32 + n0, z);
+            tmem_ld_32x32b_x1(t1 + r, y);
+            tmem_ld_32x32b_x1(t1 + 32 + r, z);
         }
         tmem_ld_wait();
-        reg_fence8(o);
-        reg_fence8(l);
+        reg_fence4(o, l, y, z);
+        float value = __uint_as_float(o), sum = __uint_as_float(l);
+        float top = split ? m0[r] : group_stats[kMax + r];
         if (split && used1) {
-            reg_fence8(y);
-            reg_fence8(z);
+            const float ma = top, mb = m1[r];
+            top = fmaxf(ma, mb);
+            const float w0 = ma == -INFINITY ? 0.f : ex2((ma - top) * sc);
+            const float w1 = mb == -INFINITY ? 0.f : ex2((mb - top) * sc);
+            sum = fmaf(__uint_as_float(z), w1, sum * w0);
+            value = fmaf(__uint_as_float(y), w1, value * w0);
         }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const int r = n0 + n;
-            if (r >= rows || (by_row && (n & (turns - 1)) != turn)) continue;
-            float value = __uint_as_float(o[n]), sum = __uint_as_float(l[n]);
-            float top = split ? m0[r] : group_stats[kMax + r];
-            if (split && used1) {
-                const float ma = top, mb = m1[r];
-                top = fmaxf(ma, mb);
-                const float w0 = ma == -INFINITY ? 0.f : ex2((ma - top) * sc);
-                const float w1 = mb == -INFINITY ? 0.f : ex2((mb - top) * sc);
-                sum = fmaf(__uint_as_float(z[n]), w1, sum * w0);
-                value = fmaf(__uint_as_float(y[n]), w1, value * w0);
-            }
-            if (row >= D) continue;
-            if (whole) {
-                const int t = r / g.group;
-                const __nv_bfloat16 b =
-                    __float2bfloat16_rn(sum == 0.f ? 0.f : __fdividef(value, sum));
-                a.out[(first_row + static_cast<long long>(t) * a.q_heads + (r - t * g.group)) * D +
-                      row] = *reinterpret_cast<const uint16_t *>(&b);
-            } else {
-                a.partial[(prow + r) * D + row] = value;
-                if (row == 0) a.stats[prow + r] = make_float2(top, sum);
-            }
+        if (row >= D) continue;
+        if (whole) {
+            const int t = r / g.group;
+            const __nv_bfloat16 b = __float2bfloat16_rn(sum == 0.f ? 0.f : __fdividef(value, sum));
+            a.out[(first_row + static_cast<long long>(t) * a.q_heads + (r - t * g.group)) * D + row] =
+                *reinterpret_cast<const uint16_t *>(&b);
+        } else {
+            a.partial[(prow + r) * D + row] = value;
+            if (row == 0) a.stats[prow + r] = make_float2(top, sum);
         }
     }
     if (flagged && row < D) {
@@ -947,8 +898,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
         const long long head_step = static_cast<long long>(D) << a.page_shift;
         const uint16_t *vc = a.v_cache + x.h * head_step + row;
         const int *table = a.table + x.r * a.max_pages;
-        for (int r = 0; r < rows; ++r) {
-            if (((by_row ? r : r >> 3) & (turns - 1)) != turn) continue;
+        for (int r = turn; r < rows; r += turns) {
             const int t = r / g.group;
             const TreeSight sight{
                 a.mask ? a.mask + static_cast<long long>(x.tok + t) * a.mask_words : nullptr,
@@ -999,10 +949,7 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
     const float sc = a.scale_log2;
     bool good = true;
     auto give_up = [&] {
-        if (lane == 0 && !*abort_flag) {
-            atomicOr(&g_status_word, kStatusEpilogueTimeout);
-            *abort_flag = 1;
-        }
+        if (lane == 0) tree_give_up(abort_flag, kStatusEpilogueTimeout);
         good = false;
     };
     auto sight = [&] {
@@ -1019,36 +966,38 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
         const bool fresh = tile == x.first;
         // the 64 scores, 32 at a time, twice: first their maximum, then the
         // weights (kept meanwhile they would be most of a thread's registers)
-        uint32_t see[2] = {~0u, ~0u};
+        const int x0 = tile * kTreeTile + 64 * half;
+        unsigned long long see = ~0ull;   // bit j: position x0 + j is seen
         if (x.edge(tile)) {
             const TreeSight t = sight();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                see[i] = row_on ? tree_visible(t, tile * kTreeTile + 64 * half + 32 * i) : 0u;
+            see = 0;
+#pragma unroll 1
+            for (int i = 32; row_on && i >= 0; i -= 32) see = see << 32 | tree_visible(t, x0 + i);
         }
         auto scores = [&](int i, uint32_t (&v)[32]) {
             tmem_ld_32x32b_x32(ts + 64 * half + 32 * i, v);
             tmem_ld_wait();
             reg_fence32(v);
-            if (see[i] != ~0u) {
+            const uint32_t bits = static_cast<uint32_t>(see >> (32 * i));
+            if (bits != ~0u) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    if (!((see[i] >> j) & 1u)) v[j] = 0xFF800000u;
+                    if (!((bits >> j) & 1u)) v[j] = 0xFF800000u;
             }
         };
         float top = -INFINITY;
         if (warp_on) {
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 uint32_t v[32];
                 scores(i, v);
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
                     mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3], fmaxf(__uint_as_float(v[j]),
                                                                      __uint_as_float(v[j + 1])));
+                top = fmaxf(fmaxf(top, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
             }
-            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         }
         const bool rise = fresh || (row_on && top * sc > m * sc + kTreeRescale);
         const bool risen = group_any(s, rise && good);
@@ -1082,7 +1031,7 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
             // no maximum so far: weights 2^(-inf - 0) = 0
             const float base = m == -INFINITY ? 0.f : -m * sc;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 uint32_t v[32], p[16];
                 scores(i, v);
@@ -1231,15 +1180,23 @@ __device__ __forceinline__ void tree_softmax(const TreeAttnArgs &a, const TreeBl
     const TreeEntry *entries = tree_entries<D>(blk.smem);
     TreePhase ph{};
     bool ok = true;
+    // rows of no request are zero
+    const int used = a.geom.requests > 0
+                         ? tree_min(tree_max(a.query_start[a.geom.requests], 0), a.geom.tokens) : 0;
+    if (used < a.geom.tokens) {
+        const long long per_token = static_cast<long long>(a.q_heads) * D / 8;
+        uint4 *o = reinterpret_cast<uint4 *>(a.out);
+#pragma unroll 1
+        for (long long i = used * per_token + blockIdx.x * (2 * kTreeGroup) + threadIdx.x;
+             i < a.geom.tokens * per_token; i += static_cast<long long>(gridDim.x) * (2 * kTreeGroup))
+            o[i] = make_uint4(0, 0, 0, 0);
+    }
     for (int seq = 0;; ++seq) {
         const int slot = seq % kTreeEntries;
         // The group's warps leave together: one that gave up comes here first,
         // so that none is left alone at a group barrier.
         ok = ok && warp_wait(bars.e_full(slot), (seq / kTreeEntries) & 1, abort_flag);
-        if (!ok && lane == 0 && !*abort_flag) {
-            atomicOr(&g_status_word, kStatusEpilogueTimeout);
-            *abort_flag = 1;
-        }
+        if (!ok && lane == 0) tree_give_up(abort_flag, kStatusEpilogueTimeout);
         if (group_any(s, !ok) || entries[slot].steps == 0) break;
         ok = NARROW ? tree_narrow_part<D>(a, blk, entries[slot], slot, ph)
                     : tree_wide_part<D>(a, blk, entries[slot], slot, ph);
@@ -1306,7 +1263,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + S::OFF_MISC);
     TreeStart *start = reinterpret_cast<TreeStart *>(smem + S::OFF_MISC + 48);
     // the prologue's sums, in the statistics' place
-    long long *warp_sums = reinterpret_cast<long long *>(tree_stats<D>(smem));
+    int2 *warp_sums = reinterpret_cast<int2 *>(tree_stats<D>(smem));
 
     if (warp == 16 && lane == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
@@ -1323,7 +1280,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         for (int i = 0; i < kTreeEntries; ++i) {
             mbar_init(bars.e_full(i), 1);
-            mbar_init(bars.e_empty(i), 17);   // the softmax warps and warp 18
+            mbar_init(bars.e_empty(i), 19);   // the softmax warps and warps 16 - 18
         }
         mbar_init(bars.both_ready(), 16);
         mbar_init(bars.o_done(), 16);
@@ -1344,78 +1301,80 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     griddep_launch_dependents();
     griddep_wait();
 
-    // ---- this block's share: sums over the requests, each thread a run of them
+    // ---- this block's share: both lines' units, summed over the requests, each
+    // thread a run of them
     auto load = [&](int r) {
         return tree_request(g, a.query_start[r], a.query_start[r + 1], a.ctx_lens[r]);
     };
-    // a request on one form's line: none of the other form's tokens
-    auto on_line = [&](int r, bool narrow) {
-        TreeReq q = load(r);
-        if (tree_is_narrow(g, q) != narrow) q.n = 0;
-        return q;
+    const int per = (g.requests + kTreeThreads - 1) / kTreeThreads;
+    const int r0 = tree_min(static_cast<int>(threadIdx.x) * per, g.requests);
+    const int r1 = tree_min(r0 + per, g.requests);
+    TreeReq q{};
+    int mine[2] = {0, 0};   // units: wide, narrow
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+        q = load(r);
+        const int u = g.kv_heads * tree_head_units(g, q);
+        if (tree_is_narrow(g, q)) mine[1] += u; else mine[0] += u;
+    }
+    // sums up to this thread, in its warp and then over the warps
+    int upto[2] = {mine[0], mine[1]};
+    auto warp_scan = [&](int (&v)[2]) {
+#pragma unroll 1
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(~0u, v[0], d), y = __shfl_up_sync(~0u, v[1], d);
+            if (lane >= d) {
+                v[0] += x;
+                v[1] += y;
+            }
+        }
     };
+    int sums[2] = {0, 0};
+    warp_scan(upto);
+    if (lane == 31) warp_sums[warp] = make_int2(upto[0], upto[1]);
+    __syncthreads();
+    if (lane < kTreeThreads / 32) {
+        sums[0] = warp_sums[lane].x;
+        sums[1] = warp_sums[lane].y;
+    }
+    warp_scan(sums);
+    const int before_w = __shfl_sync(~0u, sums[0], (warp - 1) & 31);
+    const int before_n = __shfl_sync(~0u, sums[1], (warp - 1) & 31);
+    const int wide = __shfl_sync(~0u, sums[0], 31), narrow = __shfl_sync(~0u, sums[1], 31);
+
     TreeBlock blk{};
     blk.smem = smem;
-    bool narrow = false;
-    {
-        const int per = (g.requests + kTreeThreads - 1) / kTreeThreads;
-        const int r0 = tree_min(static_cast<int>(threadIdx.x) * per, g.requests);
-        const int r1 = tree_min(r0 + per, g.requests);
-        long long units[2] = {0, 0};   // wide, narrow
-        for (int r = r0; r < r1; ++r) {
-            const TreeReq q = load(r);
-            const long long u = g.kv_heads * tree_head_units(g, q);
-            if (tree_is_narrow(g, q)) units[1] += u; else units[0] += u;
-        }
-        const TreeScan wide_scan = tree_block_scan(units[0], warp_sums);
-        const TreeScan narrow_scan = tree_block_scan(units[1], warp_sums + kTreeThreads / 32);
-        const long long nw = wide_scan.total, nn = narrow_scan.total;
-        const int lines = (nw > 0) + (nn > 0);
-        const int blocks = static_cast<int>(
-            max(static_cast<long long>(lines),
-                min(static_cast<long long>(gridDim.x), tree_div(nw + nn, a.min_units))));
-        const int nb = static_cast<int>(
-            min(static_cast<long long>(tree_narrow_blocks(nn, nw, blocks)), nn));
-        const int wb = static_cast<int>(min(static_cast<long long>(blocks - nb), nw));
-        const int c = static_cast<int>(blockIdx.x);
-        narrow = c < nb;
-        blk.base = narrow ? 0 : nb;
-        blk.index = c - blk.base;
-        const int mine_of = narrow ? nb : wb;
-        if (blk.index < mine_of) {
-            blk.cut = tree_cut(narrow ? nn : nw, mine_of);
-            const TreeScan scan = narrow ? narrow_scan : wide_scan;
-            const long long mine = units[narrow];
-            const long long u0 = tree_block_begin(blk.cut, blk.index);
-            if (u0 >= scan.before && u0 < scan.before + mine) {
-                long long at = scan.before;
-                for (int r = r0; r < r1; ++r) {
-                    const TreeReq q = on_line(r, narrow);
-                    const long long u = g.kv_heads * tree_head_units(g, q);
-                    if (u0 < at + u) {
-                        start->r = r;
-                        start->units = tree_block_begin(blk.cut, blk.index + 1) - u0;
-                        tree_locate(g, q, u0 - at, start);
-                        break;
-                    }
-                    at += u;
+    const int c = static_cast<int>(blockIdx.x);
+    const int blocks = tree_min(static_cast<int>(gridDim.x), wide + narrow);
+    const int nb = tree_min(tree_narrow_blocks(narrow, wide, blocks), narrow);
+    const int wb = tree_min(blocks - nb, wide);
+    const bool is_narrow = c < nb;
+    blk.base = is_narrow ? 0 : nb;
+    blk.index = c - blk.base;
+    if (blk.index < (is_narrow ? nb : wb)) {
+        blk.cut = is_narrow ? tree_cut(narrow, nb) : tree_cut(wide, wb);
+        const int u0 = tree_block_begin(blk.cut, blk.index);
+        const int own = is_narrow ? mine[1] : mine[0];
+        int at = (is_narrow ? upto[1] + (warp ? before_n : 0) : upto[0] + (warp ? before_w : 0)) - own;
+        if (u0 >= at && u0 < at + own) {
+#pragma unroll 1
+            for (int r = r0; r < r1; ++r) {
+                if (per > 1) q = load(r);
+                if (tree_is_narrow(g, q) != is_narrow) continue;
+                const int per_head = tree_head_units(g, q);
+                if (u0 < at + g.kv_heads * per_head) {
+                    start->r = r;
+                    start->units = tree_block_begin(blk.cut, blk.index + 1) - u0;
+                    tree_locate(g, q, u0 - at, per_head, start);
+                    break;
                 }
+                at += g.kv_heads * per_head;
             }
         }
     }
-    // rows of no request are zero
-    {
-        const int used = g.requests > 0
-                             ? tree_min(tree_max(a.query_start[g.requests], 0), g.tokens) : 0;
-        const long long per_token = static_cast<long long>(a.q_heads) * D / 8;
-        uint4 *o = reinterpret_cast<uint4 *>(a.out);
-        for (long long i = used * per_token + blockIdx.x * kTreeThreads + threadIdx.x;
-             i < g.tokens * per_token; i += static_cast<long long>(gridDim.x) * kTreeThreads)
-            o[i] = make_uint4(0, 0, 0, 0);
-    }
     // (the sums above have passed block barriers: the address is there)
     blk.tmem = *tmem_holder;
-    if (narrow && warp < 4) {
+    if (is_narrow && warp < 4) {
         uint32_t ones[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) ones[i] = 0x3F803F80u;   // BF16 pairs
@@ -1426,10 +1385,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (narrow)
-        tree_block<D, true>(tmQn, tmK, tmV, a, blk, *start, [&](int r) { return on_line(r, true); });
+    // a request on one form's line: none of the other form's tokens
+    auto on_line = [&](int r) {
+        TreeReq x = load(r);
+        if (tree_is_narrow(g, x) != is_narrow) x.n = 0;
+        return x;
+    };
+    if (is_narrow)
+        tree_block<D, true>(tmQn, tmK, tmV, a, blk, *start, on_line);
     else
-        tree_block<D, false>(tmQ, tmK, tmV, a, blk, *start, [&](int r) { return on_line(r, false); });
+        tree_block<D, false>(tmQ, tmK, tmV, a, blk, *start, on_line);
     if (warp == 17) {
         __syncwarp();
         tc_fence_after();

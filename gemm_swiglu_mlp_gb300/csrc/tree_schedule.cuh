@@ -17,8 +17,10 @@
 
 #ifdef __CUDACC__
 #define SWIGLU_HD __host__ __device__ __forceinline__
+#define SWIGLU_HD_CALL __host__ __device__ __noinline__
 #else
 #define SWIGLU_HD inline
+#define SWIGLU_HD_CALL inline
 #endif
 
 namespace swiglu {
@@ -27,11 +29,22 @@ constexpr int kTreeTile = 128;   // positions a tile, and rows of a row tile
 
 struct TreeGeom {
     int requests, tokens, kv_heads;
-    int group;      // query heads per kv head, 1..128
-    int tpt;        // tokens per row tile, 128 / group
-    int causal;     // 1: no mask, a token sees the new tokens up to itself
-    int max_rows;   // positions a block-table row can hold
+    int group;        // query heads per kv head, 1..128
+    int tpt;          // tokens per row tile, 128 / group
+    uint32_t recip;   // ceil(2^32 / (2 * tpt)): n / (2 * tpt) for n < 2^24
+    int causal;       // 1: no mask, a token sees the new tokens up to itself
+    int max_rows;     // positions a block-table row can hold
 };
+// Limits that keep every unit count in 32 bits (checked on the host):
+// tokens below 2^24, and this bound on the units of one call.
+SWIGLU_HD uint32_t tree_recip(int tpt) {
+    return static_cast<uint32_t>(((1ull << 32) + 2 * tpt - 1) / (2 * tpt));
+}
+inline bool tree_fits(const TreeGeom &g) {
+    const double items = static_cast<double>(g.tokens) / (2 * g.tpt) + g.requests;
+    return g.tokens < (1 << 24) &&
+           items * g.kv_heads * (g.max_rows / kTreeTile + 1.0) < 2147483648.0;
+}
 
 struct TreeReq {
     int t0;    // first token
@@ -57,23 +70,17 @@ SWIGLU_HD TreeReq tree_request(const TreeGeom &g, int start, int end, int ctx) {
 // has a line of work with only its requests on it.
 constexpr int kTreeNarrow = 32;
 SWIGLU_HD bool tree_is_narrow(const TreeGeom &g, const TreeReq &q) {
-    return static_cast<long long>(q.n) * g.group <= kTreeNarrow;
+    return q.n <= kTreeNarrow && q.n * g.group <= kTreeNarrow;
 }
 
 SWIGLU_HD int tree_items(const TreeGeom &g, const TreeReq &q) {
-    return (q.n + 2 * g.tpt - 1) / (2 * g.tpt);
+    return static_cast<int>(
+        (static_cast<uint64_t>(static_cast<uint32_t>(q.n + 2 * g.tpt - 1)) * g.recip) >> 32);
 }
 
-// Tokens of item `item` of a request.
-SWIGLU_HD int tree_item_tokens(const TreeGeom &g, const TreeReq &q, int item) {
-    return tree_min(2 * g.tpt, q.n - item * 2 * g.tpt);
-}
-
-// Positions that some token of the item may see (>= 1).
+// Positions that some token of item `item` may see (>= 1).
 SWIGLU_HD int tree_item_len(const TreeGeom &g, const TreeReq &q, int item) {
-    const int upto = g.causal ? tree_min(q.n, (item + 1) * 2 * g.tpt) : q.n;
-    const long long len = static_cast<long long>(q.ctx) + upto;
-    return len < g.max_rows ? static_cast<int>(len) : g.max_rows;
+    return tree_min(q.ctx + (g.causal ? tree_min(q.n, (item + 1) * 2 * g.tpt) : q.n), g.max_rows);
 }
 
 SWIGLU_HD int tree_item_tiles(const TreeGeom &g, const TreeReq &q, int item) {
@@ -81,70 +88,57 @@ SWIGLU_HD int tree_item_tiles(const TreeGeom &g, const TreeReq &q, int item) {
 }
 
 // Units of one kv head of a request.
-SWIGLU_HD long long tree_head_units(const TreeGeom &g, const TreeReq &q) {
+SWIGLU_HD_CALL int tree_head_units(const TreeGeom &g, const TreeReq &q) {
     const int items = tree_items(g, q);
-    if (!g.causal) return items ? static_cast<long long>(items) * tree_item_tiles(g, q, 0) : 0;
-    long long u = 0;
+    if (!g.causal) return items * tree_item_tiles(g, q, 0);
+    int u = 0;
     for (int i = 0; i < items; ++i) u += tree_item_tiles(g, q, i);
     return u;
 }
 
-// a / b for a >= 0, b > 0: nearly every a fits 32 bits, whose division is
-// several times cheaper on the GPU.
-SWIGLU_HD long long tree_div(long long a, int b) {
-    if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-// The line of `total` units cut for `blocks` blocks: the first `more` of them
-// take one unit above `each`.
-struct TreeCut {
-    long long each;
-    int more;
-};
-SWIGLU_HD TreeCut tree_cut(long long total, int blocks) {
-    TreeCut c;
-    c.each = tree_div(total, blocks);
-    c.more = static_cast<int>(total - c.each * blocks);
-    return c;
-}
-SWIGLU_HD long long tree_block_begin(const TreeCut &c, int block) {
-    return c.each * block + tree_min(block, c.more);
-}
-// Block that does unit u (each >= 1).
-SWIGLU_HD int tree_block_of(const TreeCut &c, long long u) {
-    const long long fat = (c.each + 1) * c.more;
-    return static_cast<int>(u < fat ? u / (c.each + 1) : c.more + (u - fat) / c.each);
-}
-
-// How many of `blocks` (>= 2 where both lines have work) blocks take the narrow form's line: in proportion to
-// the units, a wide tile counted as kTreeWideCost / 4 narrow ones (a
-// narrow tile's time is its bytes', a wide one's also its products').
+// How many of `blocks` (>= 2 where both lines have work) blocks take the narrow
+// form's line: in proportion to the units, a wide tile counted as
+// kTreeWideCost / 4 narrow ones (a narrow tile's time is its bytes', a wide
+// one's also its products').
 constexpr int kTreeWideCost = 6;
-SWIGLU_HD int tree_narrow_blocks(long long narrow, long long wide, int blocks) {
+SWIGLU_HD int tree_narrow_blocks(int narrow, int wide, int blocks) {
     if (narrow == 0) return 0;
     if (wide == 0) return blocks;
-    while (((narrow | wide) >> 20) != 0) {   // keep the products in 32 bits
-        narrow = (narrow + 1) >> 1;
-        wide = (wide + 1) >> 1;
-    }
-    const uint32_t a = static_cast<uint32_t>(narrow) * 4, b = static_cast<uint32_t>(wide) * kTreeWideCost;
-    const int n = static_cast<int>((static_cast<uint64_t>(a) * blocks + (a + b) / 2) / (a + b));
+    const float a = 4.f * static_cast<float>(narrow), b = kTreeWideCost * static_cast<float>(wide);
+    const int n = static_cast<int>(blocks * (a / (a + b)) + 0.5f);
     return tree_max(1, tree_min(n, blocks - 1));
+}
+
+// A line of `total` units cut for `blocks` <= total blocks: the first `more`
+// of them take one unit above `each`.
+struct TreeCut {
+    int each, more;
+};
+SWIGLU_HD TreeCut tree_cut(int total, int blocks) {
+    TreeCut c;
+    c.each = static_cast<int>(static_cast<uint32_t>(total) / static_cast<uint32_t>(blocks));
+    c.more = total - c.each * blocks;
+    return c;
+}
+SWIGLU_HD int tree_block_begin(const TreeCut &c, int block) {
+    return c.each * block + tree_min(block, c.more);
+}
+// Block that does unit u.
+SWIGLU_HD int tree_block_of(const TreeCut &c, int u) {
+    const int fat = (c.each + 1) * c.more;
+    return u < fat ? u / (c.each + 1) : c.more + (u - fat) / c.each;
 }
 
 // Where a block begins: `tile` of item (r, h, item), `units` tiles to do.
 struct TreeStart {
-    int r, h, item, tile;
-    long long units;
+    TreeReq q;
+    int r, h, item, tile, units;
 };
 
 // The place `rem` units into request r.
-SWIGLU_HD void tree_locate(const TreeGeom &g, const TreeReq &q, long long rem, TreeStart *s) {
-    const long long per_head = tree_head_units(g, q);
-    s->h = static_cast<int>((rem >> 32) == 0 && (per_head >> 32) == 0
-                                ? static_cast<uint32_t>(rem) / static_cast<uint32_t>(per_head)
-                                : rem / per_head);
+SWIGLU_HD void tree_locate(const TreeGeom &g, const TreeReq &q, int rem, int per_head, TreeStart *s) {
+    s->q = q;
+    s->h = static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(per_head));
     rem -= s->h * per_head;
     int item = 0;
     while (true) {
@@ -154,7 +148,7 @@ SWIGLU_HD void tree_locate(const TreeGeom &g, const TreeReq &q, long long rem, T
         ++item;
     }
     s->item = item;
-    s->tile = static_cast<int>(rem);
+    s->tile = rem;
 }
 
 // TreePart::flags
@@ -167,27 +161,27 @@ enum : int {
 // One softmax group's part in an entry (below): a row tile and the tiles
 // first, first + stride, .. (< end) of its item.
 struct TreePart {
+    int first, stride, end;
+    int edge_from;    // min(ctx, len): tiles that reach past it need a look (new
+                      // tokens, or past the end)
     int r, h;         // request, kv head
     int tok;          // first token of the row tile (row of q)
     int place;        // its place among the request's new tokens
     int ntok;         // tokens of the row tile
     int ctx, len;     // of the request; positions of the item
-    int first, stride, end;
     int flags;
 
     SWIGLU_HD bool used() const { return first < end; }
     SWIGLU_HD bool active(int step) const { return first + step * stride < end; }
     SWIGLU_HD int tile(int step) const { return first + step * stride; }
-    SWIGLU_HD bool last(int step) const { return first + (step + 1) * stride >= end; }
-    // a tile with positions that need a look: new tokens, or past the end
-    SWIGLU_HD bool edge(int t) const { return (t + 1) * kTreeTile > tree_min(ctx, len); }
+    SWIGLU_HD bool edge(int t) const { return (t + 1) * kTreeTile > edge_from; }
 };
+
 // What both groups do next. kTreeSplit: an item of one row tile, the groups
 // take its even and odd tiles and merge their results. kTreePair: an item of
 // two row tiles, one a group, over the same tiles. kTreeDuo: two short items
 // of one row tile each, one a group; while one group's softmax or result runs,
-// the tensor cores work for the other (kTreeDuoTiles: 608 one-tile items on
-// 152 blocks, see the kernel).
+// the tensor cores work for the other.
 enum : int { kTreeSplit = 0, kTreePair = 1, kTreeDuo = 2 };
 constexpr int kTreeDuoTiles = 4;
 struct TreeEntry {
@@ -195,7 +189,10 @@ struct TreeEntry {
     int kind;
     int steps;        // 0: nothing left
     SWIGLU_HD bool two_q() const { return kind != kTreeSplit; }    // a Q tile a group
-    SWIGLU_HD bool two_kv() const { return kind != kTreePair; }    // K and V tiles a group
+    // group s has a K and a V tile of its own in a step
+    SWIGLU_HD bool own_kv(int step, int s) const {
+        return part[s].active(step) && (s == 0 || kind != kTreePair);
+    }
 };
 
 // The items of one block in order.
@@ -204,32 +201,28 @@ struct TreeWalk {
     int r, h, item, items;
     int tokens, len, tiles;   // of the item
     int tb, te;               // this block's tiles of it
-    long long left;           // units left, this item's included
+    int left;                 // units left, this item's included
 
-    SWIGLU_HD bool valid() const { return left > 0; }
     SWIGLU_HD bool pair(const TreeGeom &g) const { return tokens > g.tpt; }
-    SWIGLU_HD int item_token0(const TreeGeom &g) const { return item * 2 * g.tpt; }
 
     SWIGLU_HD void set_item(const TreeGeom &g, int from) {
-        tokens = tree_item_tokens(g, q, item);
+        tokens = tree_min(2 * g.tpt, q.n - item * 2 * g.tpt);
         len = tree_item_len(g, q, item);
         tiles = (len + kTreeTile - 1) / kTreeTile;
         tb = from;
-        te = static_cast<int>(left < tiles - from ? from + left : tiles);
+        te = tree_min(tiles, from + left);
     }
-    template <typename Load>   // Load(r) -> TreeReq
-    SWIGLU_HD void begin(const TreeGeom &g, const TreeStart &s, Load load) {
+    SWIGLU_HD void begin(const TreeGeom &g, const TreeStart &s) {
+        q = s.q;
         r = s.r;
         h = s.h;
         item = s.item;
         left = s.units;
-        if (left <= 0) return;
-        q = load(r);
         items = tree_items(g, q);
         set_item(g, s.tile);
     }
     // The next item, or left = 0.
-    template <typename Load>
+    template <typename Load>   // Load(r) -> TreeReq, n = 0: not on this line
     SWIGLU_HD void next(const TreeGeom &g, Load load) {
         left -= te - tb;
         if (left <= 0) return;
@@ -237,64 +230,66 @@ struct TreeWalk {
             item = 0;
             if (++h == g.kv_heads) {
                 h = 0;
-                do q = load(++r);
-                while (q.n == 0);
+                do {
+                    if (++r >= g.requests) {   // (never on a line that was counted right)
+                        left = 0;
+                        return;
+                    }
+                    q = load(r);
+                } while (q.n == 0);
                 items = tree_items(g, q);
             }
         }
         set_item(g, 0);
     }
-    SWIGLU_HD TreePart part(const TreeGeom &g, int rt, int first, int stride) const {
+    SWIGLU_HD TreePart part(const TreeGeom &g) const {
         TreePart p;
         p.r = r;
         p.h = h;
-        p.place = item_token0(g) + rt * g.tpt;
+        p.place = item * 2 * g.tpt;
         p.tok = q.t0 + p.place;
-        p.ntok = tree_min(g.tpt, tokens - rt * g.tpt);
+        p.ntok = tree_min(g.tpt, tokens);
         p.ctx = q.ctx;
         p.len = len;
-        p.first = first;
-        p.stride = stride;
+        p.edge_from = tree_min(q.ctx, len);
+        p.first = tb;
+        p.stride = 1;
         p.end = te;
-        p.flags = (tb == 0 && te == tiles ? kPartWhole : 0) | (tb == 0 ? kPartBegins : 0) |
-                  (rt ? kPartSecond : 0);
+        p.flags = (tb == 0 && te == tiles ? kPartWhole : 0) | (tb == 0 ? kPartBegins : 0);
         return p;
     }
     // The next entry; moves on past its items. steps = 0 at the end.
     template <typename Load>
-    SWIGLU_HD TreeEntry entry(const TreeGeom &g, Load load) {
-        TreeEntry e;
-        e.kind = kTreeSplit;
-        e.steps = 0;
-        if (!valid()) return e;
+    SWIGLU_HD void entry(const TreeGeom &g, Load load, TreeEntry *e) {
+        e->kind = kTreeSplit;
+        e->steps = 0;
+        if (left <= 0) return;
         const int mine = te - tb;
-        if (pair(g)) {
-            e.kind = kTreePair;
-            e.steps = mine;
-            e.part[0] = part(g, 0, tb, 1);
-            e.part[1] = part(g, 1, tb, 1);
-            next(g, load);
-            return e;
+        const bool two = pair(g);
+        TreePart p = part(g);
+        e->part[0] = p;
+        if (two) {
+            e->kind = kTreePair;
+            e->steps = mine;
+            p.place += g.tpt;
+            p.tok += g.tpt;
+            p.ntok = tokens - g.tpt;
+            p.flags |= kPartSecond;
         }
-        if (mine <= kTreeDuoTiles && left > mine) {
-            e.part[0] = part(g, 0, tb, 1);
-            next(g, load);
-            if (!pair(g) && te - tb <= kTreeDuoTiles) {
-                e.kind = kTreeDuo;
-                e.part[1] = part(g, 0, tb, 1);
-                e.steps = tree_max(mine, te - tb);
+        next(g, load);
+        if (!two) {
+            if (mine <= kTreeDuoTiles && left > 0 && !pair(g) && te - tb <= kTreeDuoTiles) {
+                e->kind = kTreeDuo;
+                e->steps = tree_max(mine, te - tb);
+                p = part(g);
                 next(g, load);
-                return e;
+            } else {
+                e->steps = (mine + 1) / 2;
+                e->part[0].stride = p.stride = 2;
+                p.first += 1;
             }
-        } else {
-            e.part[0] = part(g, 0, tb, 1);
-            next(g, load);
         }
-        e.part[1] = e.part[0];
-        e.part[1].first += 1;
-        e.part[0].stride = e.part[1].stride = 2;
-        e.steps = (mine + 1) / 2;
-        return e;
+        e->part[1] = p;
     }
 };
 

@@ -24,12 +24,23 @@ int main(int argc, char **argv) {
     const int cases = argc > 1 ? std::atoi(argv[1]) : 400;
     std::mt19937 rng(7);
     auto pick = [&](int lo, int hi) { return lo + static_cast<int>(rng() % (hi - lo + 1)); };
+    for (int tpt = 1, it = 0; tpt <= 128; ++tpt) {   // the division by 2 * tpt
+        TreeGeom g{};
+        g.tpt = tpt;
+        g.recip = tree_recip(tpt);
+        for (int n : {0, 1, 2 * tpt - 1, 2 * tpt, 2 * tpt + 1, 999983, (1 << 24) - 1,
+                      (1 << 24) / (2 * tpt) * (2 * tpt) - 1, ((1 << 24) - 1) / (2 * tpt) * (2 * tpt)}) {
+            const TreeReq q{0, n, 0};
+            CHECK(tree_items(g, q) == (n + 2 * tpt - 1) / (2 * tpt));
+        }
+    }
     for (int it = 0; it < cases; ++it) {
         TreeGeom g{};
         g.requests = pick(1, it % 5 == 0 ? 300 : 12);
         g.kv_heads = pick(1, 8);
         g.group = it % 7 == 0 ? 128 : pick(1, 12);
         g.tpt = 128 / g.group;
+        g.recip = tree_recip(g.tpt);
         g.causal = pick(0, 1);
         g.max_rows = 16 * pick(1, it % 3 ? 40 : 2000);
         std::vector<int> start{0}, ctx;
@@ -39,22 +50,29 @@ int main(int argc, char **argv) {
         }
         g.tokens = start.back() - (it % 11 == 0 ? pick(0, 2) : 0);   // sometimes cut short
         if (g.tokens < 0) g.tokens = 0;
-        auto load = [&](int r) { return tree_request(g, start[r], start[r + 1], ctx[r]); };
-        long long total = 0;
-        std::vector<long long> before;
+        // one of the two lines, as the kernel's loads see it
+        const bool narrow = pick(0, 1) != 0;
+        auto load = [&](int r) {
+            TreeReq q = tree_request(g, start[r], start[r + 1], ctx[r]);
+            if (tree_is_narrow(g, q) != narrow) q.n = 0;
+            return q;
+        };
+        CHECK(tree_fits(g));
+        int total = 0;
+        std::vector<int> before;
         for (int r = 0; r < g.requests; ++r) {
             before.push_back(total);
             total += g.kv_heads * tree_head_units(g, load(r));
         }
         if (total == 0) continue;
-        const int blocks = static_cast<int>(total < 152 ? pick(1, static_cast<int>(total)) : 152);
+        const int blocks = total < 152 ? pick(1, total) : 152;
         std::map<std::tuple<int, int, int>, int> done;   // tiles done so far of an item
         std::map<std::tuple<int, int, int>, std::pair<int, int>> by;   // first and last block
         std::map<std::tuple<int, int, int>, int> says;   // last block as the first one says
         const TreeCut cut = tree_cut(total, blocks);
-        long long units = 0;
+        int units = 0;
         for (int c = 0; c < blocks; ++c) {
-            const long long u0 = tree_block_begin(cut, c), u1 = tree_block_begin(cut, c + 1);
+            const int u0 = tree_block_begin(cut, c), u1 = tree_block_begin(cut, c + 1);
             CHECK(u1 > u0 && u1 <= total);
             CHECK(tree_block_of(cut, u0) == c && tree_block_of(cut, u1 - 1) == c);
             int r = 0;
@@ -63,13 +81,14 @@ int main(int argc, char **argv) {
             TreeStart s{};
             s.r = r;
             s.units = u1 - u0;
-            tree_locate(g, load(r), u0 - before[r], &s);
+            tree_locate(g, load(r), u0 - before[r], tree_head_units(g, load(r)), &s);
             TreeWalk w{};
-            w.begin(g, s, load);
-            long long u = u0;
+            w.begin(g, s);
+            int u = u0;
             while (true) {
-                const TreeWalk at = w;
-                const TreeEntry e = w.entry(g, load);
+                const TreeWalk at = w;   // before the entry
+                TreeEntry e{};
+                w.entry(g, load, &e);
                 if (e.steps == 0) break;
                 const int items = e.kind == kTreeDuo ? 2 : 1;
                 for (int k = 0; k < items; ++k) {
@@ -108,8 +127,7 @@ int main(int argc, char **argv) {
                         if (e.part[k].active(st)) {
                             seen[k].push_back(e.part[k].tile(st));
                             CHECK(e.part[k].used());
-                            CHECK(e.part[k].last(st) ==
-                                  (e.part[k].tile(st) + e.part[k].stride >= e.part[k].end));
+                            CHECK(e.own_kv(st, k) == (k == 0 || e.kind != kTreePair));
                         }
                 for (int k = 0; k < 2; ++k) {
                     CHECK(!e.part[k].active(e.steps));
