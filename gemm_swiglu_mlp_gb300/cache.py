@@ -22,12 +22,20 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (SWIGLU_ERR_INVALID_ARG, SwigluError, _check, _OnDevice, _out_tensor,
-               _require_bf16_cuda, _stream_handle, load_library)
+from . import SWIGLU_ERR_INVALID_ARG, SWIGLU_OK, SwigluError, load_library
+
+# These calls are a few microseconds of GPU time in a serving step, so the
+# binding keeps its own small: one comparison per tensor on the way that
+# succeeds (what is wrong is worked out only for the message), and the current
+# stream's handle without a Stream object (~3 us).
+_I32, _I64, _BF16 = torch.int32, torch.int64, torch.bfloat16
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 # (device index, stream handle) -> uint8 tensor; apart from the other entry
 # points' workspaces, whose counters have to stay as they are between calls
 _workspaces = {}
+_ws_bytes = {}     # (device index, tokens, q heads, kv heads, head size) -> bytes
 
 
 class CachePlan(NamedTuple):
@@ -40,55 +48,80 @@ class CachePlan(NamedTuple):
     mask: Optional[torch.Tensor]       # [max_tokens, words] int64, or None
 
 
-def _require_ints(t, name: str, device, shape, dtype=torch.int32):
-    """An int32 (or `dtype`) CUDA tensor on `device`, contiguous, of `shape`
-    (None: any extent)."""
+def _refuse(t, name: str, index: int, dtype, shape, contiguous=True):
+    """Says what is wrong with a tensor that one of the checks below refused."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    got = t.shape
-    if len(got) != len(shape) or any(b is not None and a != b for a, b in zip(got, shape)):
-        raise ValueError("%s must be %s, got %s" % (
-            name, [("any" if b is None else b) for b in shape], list(got)))
-    if not t.is_contiguous():
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
+    if contiguous and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be %s, got %s" % (name, shape, list(t.shape)))
 
 
-def _require_rows(t, name: str, device, heads=None, dim=None):
-    """A [tokens, heads, head size] BF16 view: any strides of the first two
-    dimensions that are multiples of 8, the last one contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype is not torch.bfloat16:
-        raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    shape = t.shape
-    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (
-            dim is not None and shape[2] != dim):
-        raise ValueError("%s must be [tokens, %s, %s], got %s" % (
-            name, "heads" if heads is None else heads, "head size" if dim is None else dim,
-            list(shape)))
-    s = t.stride()
-    if s[2] != 1 or s[0] % 8 or s[1] % 8:
-        raise ValueError("%s must have a contiguous last dimension and strides that are "
-                         "multiples of 8, got strides %s" % (name, s))
-    return s
+def _vector(t, name: str, n, index: int):
+    """A contiguous int32 CUDA vector of n values (None: any) on device
+    `index` (-1: any); returns its length and device."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _I32 and t.is_contiguous():
+        shape, at = t.shape, t.get_device()
+        if len(shape) == 1 and (n is None or shape[0] == n) and (index < 0 or at == index):
+            return shape[0], at
+    _refuse(t, name, index if index >= 0 else 0, _I32, "[%s]" % ("any" if n is None else n))
 
 
-def _require_caches(k_cache, v_cache, layered: bool):
-    _require_bf16_cuda(k_cache, "k_cache")
-    _require_bf16_cuda(v_cache, "v_cache")
-    dims = k_cache.dim()
-    if (dims != 4 and not (layered and dims == 5)) or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must both be [%spages, kv heads, page size, "
-                         "head size]" % ("layers, " if layered and dims == 5 else ""))
-    if v_cache.device != k_cache.device:
-        raise ValueError("v_cache must be on %s" % k_cache.device)
-    return k_cache.shape
+def _matrix(t, name: str, rows: int, index: int, dtype=_I32) -> int:
+    """A contiguous CUDA matrix of `rows` rows; returns its columns (>= 1)."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and t.get_device() == index):
+        shape = t.shape
+        if len(shape) == 2 and shape[0] == rows and shape[1] > 0:
+            return shape[1]
+    _refuse(t, name, index, dtype, "[%d, at least 1]" % rows)
+
+
+def _rows(t, name: str, index: int, tokens, heads, dim: int):
+    """A [tokens, heads, dim] BF16 view (None: any) whose last dimension is
+    contiguous, any strides of the others that are multiples of 8; returns
+    (shape, strides)."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _BF16
+            and t.get_device() == index):
+        shape = t.shape
+        if (len(shape) == 3 and shape[2] == dim and (heads is None or shape[1] == heads)
+                and (tokens is None or shape[0] == tokens)):
+            s = t.stride()
+            if s[2] == 1 and not (s[0] | s[1]) & 7:
+                return shape, s
+            raise ValueError("%s must have a contiguous last dimension and strides that are "
+                             "multiples of 8, got strides %s" % (name, s))
+    _refuse(t, name, index, _BF16, "[%s, %s, %d]" % (
+        "tokens" if tokens is None else tokens, "heads" if heads is None else heads, dim), False)
+
+
+def _caches(k_cache, v_cache, layered: bool):
+    """(shape, device index) of a pair of caches."""
+    if (isinstance(k_cache, torch.Tensor) and k_cache.is_cuda and k_cache.dtype is _BF16
+            and k_cache.is_contiguous()):
+        shape, index = k_cache.shape, k_cache.get_device()
+        if len(shape) == 4 or (layered and len(shape) == 5):
+            if (isinstance(v_cache, torch.Tensor) and v_cache.is_cuda and v_cache.dtype is _BF16
+                    and v_cache.is_contiguous() and v_cache.shape == shape
+                    and v_cache.get_device() == index):
+                return shape, index
+            _refuse(v_cache, "v_cache", index, _BF16, list(shape))
+    _refuse(k_cache, "k_cache", k_cache.get_device() if isinstance(k_cache, torch.Tensor) else 0,
+            _BF16, "[%spages, kv heads, page size, head size]" % ("layers, " if layered else ""))
+
+
+def _call(entry: str, fn, index: int, stream, *args):
+    """fn(*args, stream handle) with device `index` current."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call(entry, fn, index, stream, *args)
+    status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if status != SWIGLU_OK:
+        raise SwigluError(status, entry)
 
 
 def swiglu_cache_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, pages_held: torch.Tensor,
@@ -101,51 +134,45 @@ def swiglu_cache_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, pages_held
     `max_tokens` rows of slots, positions and masks are made (rows past the
     step's tokens: slot -1, mask 0). `free_head` [1] (None: 0) is where the
     free list starts; the next step's is counts[2:3]."""
-    lib = load_library()
-    dev = ctx_lens.device if isinstance(ctx_lens, torch.Tensor) else None
-    _require_ints(ctx_lens, "ctx_lens", dev, (None,))
-    R = ctx_lens.shape[0]
-    max_tokens = int(max_tokens)
-    _require_ints(new_lens, "new_lens", dev, (R,))
-    _require_ints(pages_held, "pages_held", dev, (R,))
-    _require_ints(block_table, "block_table", dev, (R, None))
-    _require_ints(free_pages, "free_pages", dev, (None,))
+    R, index = _vector(ctx_lens, "ctx_lens", None, -1)
+    T = int(max_tokens)
+    _vector(new_lens, "new_lens", R, index)
+    _vector(pages_held, "pages_held", R, index)
+    if R or block_table.dim() != 2:
+        max_pages = _matrix(block_table, "block_table", R, index)
+    else:
+        max_pages = max(block_table.shape[1], 1)
+    num_free, _ = _vector(free_pages, "free_pages", None, index)
+    head_ptr = par_ptr = mask_ptr = None
     if free_head is not None:
-        _require_ints(free_head, "free_head", dev, (1,))
+        _vector(free_head, "free_head", 1, index)
+        head_ptr = free_head.data_ptr()
     width = words = 0
     if parents is not None:
-        _require_ints(parents, "parents", dev, (R, None))
-        width = parents.shape[1]
+        width = _matrix(parents, "parents", R, index)
         words = (width + 63) // 64
-        if width == 0:
-            raise ValueError("parents must have at least one column")
+        par_ptr = parents.data_ptr()
     if out is None:
-        i32 = {"dtype": torch.int32, "device": dev}
-        out = CachePlan(torch.empty(R + 1, **i32), torch.empty(max_tokens, **i32),
-                        torch.empty(max_tokens, **i32), torch.empty(R, **i32),
-                        torch.empty(3, **i32),
-                        None if parents is None else torch.empty(
-                            (max_tokens, words), dtype=torch.int64, device=dev))
+        new = ctx_lens.new_empty
+        out = CachePlan(new((R + 1,)), new((T,)), new((T,)), new((R,)), new((3,)),
+                        None if parents is None else new((T, words), dtype=_I64))
     else:
-        _require_ints(out.query_start, "out.query_start", dev, (R + 1,))
-        _require_ints(out.slots, "out.slots", dev, (max_tokens,))
-        _require_ints(out.positions, "out.positions", dev, (max_tokens,))
-        _require_ints(out.pages_held, "out.pages_held", dev, (R,))
-        _require_ints(out.counts, "out.counts", dev, (3,))
+        _vector(out.query_start, "out.query_start", R + 1, index)
+        _vector(out.slots, "out.slots", T, index)
+        _vector(out.positions, "out.positions", T, index)
+        _vector(out.pages_held, "out.pages_held", R, index)
+        _vector(out.counts, "out.counts", 3, index)
         if (out.mask is None) != (parents is None):
             raise ValueError("out.mask goes with parents: both or neither")
-        if parents is not None:
-            _require_ints(out.mask, "out.mask", dev, (max_tokens, words), torch.int64)
-    with _OnDevice(dev):
-        _check(lib.swiglu_cache_plan(
-            ctx_lens.data_ptr(), new_lens.data_ptr(), pages_held.data_ptr(),
-            block_table.data_ptr(), R, block_table.shape[1], free_pages.data_ptr(),
-            free_pages.shape[0], None if free_head is None else free_head.data_ptr(),
-            int(page_size), None if parents is None else parents.data_ptr(), width, max_tokens,
-            out.query_start.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
-            out.pages_held.data_ptr(), out.counts.data_ptr(),
-            None if parents is None else out.mask.data_ptr(), _stream_handle(stream)),
-            "swiglu_cache_plan")
+    if parents is not None:
+        if T and _matrix(out.mask, "out.mask", T, index, _I64) != words:
+            raise ValueError("out.mask must be [%d, %d]" % (T, words))
+        mask_ptr = out.mask.data_ptr()
+    _call("swiglu_cache_plan", load_library().swiglu_cache_plan, index, stream,
+          ctx_lens.data_ptr(), new_lens.data_ptr(), pages_held.data_ptr(), block_table.data_ptr(),
+          R, max_pages, free_pages.data_ptr(), num_free, head_ptr, int(page_size), par_ptr, width,
+          T, out.query_start.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+          out.pages_held.data_ptr(), out.counts.data_ptr(), mask_ptr)
     return out
 
 
@@ -153,20 +180,14 @@ def swiglu_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                        k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
     """Rows of k and v [tokens, kv heads, head size] (strided views allowed)
     into the caches, row t at slots[t]; rows with a negative slot are dropped."""
-    lib = load_library()
-    pages, heads, page_size, dim = _require_caches(k_cache, v_cache, False)
-    dev = k_cache.device
-    ks = _require_rows(k, "k", dev, heads, dim)
-    vs = _require_rows(v, "v", dev, heads, dim)
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError("k and v must have the same number of tokens")
-    _require_ints(slots, "slots", dev, (T,))
-    with _OnDevice(dev):
-        _check(lib.swiglu_cache_write(
-            k.data_ptr(), v.data_ptr(), T, heads, dim, ks[0], ks[1], vs[0], vs[1],
-            slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
-            _stream_handle(stream)), "swiglu_cache_write")
+    (pages, heads, page_size, dim), index = _caches(k_cache, v_cache, False)
+    shape, ks = _rows(k, "k", index, None, heads, dim)
+    T = shape[0]
+    _, vs = _rows(v, "v", index, T, heads, dim)
+    _vector(slots, "slots", T, index)
+    _call("swiglu_cache_write", load_library().swiglu_cache_write, index, stream,
+          k.data_ptr(), v.data_ptr(), T, heads, dim, ks[0], ks[1], vs[0], vs[1], slots.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size)
 
 
 def swiglu_tree_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int,
@@ -175,11 +196,10 @@ def swiglu_tree_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: i
         int(tokens), int(q_heads), int(kv_heads), int(head_dim)))
 
 
-def _workspace(device, nbytes: int, stream) -> torch.Tensor:
+def _workspace(index: int, nbytes: int, stream) -> torch.Tensor:
     """One attention workspace per (device, stream), grown on demand."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    key = (device.index, int(s.cuda_stream))
-    ws = _workspaces.get(key)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    ws = _workspaces.get((index, handle))
     if ws is None or ws.numel() < nbytes:
         if torch.cuda.is_current_stream_capturing():
             # an allocation made during capture belongs to the graph's pool
@@ -187,9 +207,9 @@ def _workspace(device, nbytes: int, stream) -> torch.Tensor:
                               "this call needs a workspace of %d bytes: allocate it before "
                               "capturing (swiglu_tree_attention_workspace_bytes) and pass "
                               "workspace=" % nbytes)
-        with torch.cuda.stream(s):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        _workspaces[index, handle] = ws
     return ws
 
 
@@ -203,37 +223,41 @@ def swiglu_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     context and the new tokens in its row of `mask` [tokens, words] int64
     (None: those before it, and itself). The step's own keys and values are
     in the cache already (swiglu_cache_write). `scale` None: 1/sqrt(head size)."""
-    lib = load_library()
-    pages, kv_heads, page_size, dim = _require_caches(k_cache, v_cache, False)
-    dev = k_cache.device
-    qs = _require_rows(q, "q", dev, None, dim)
-    T, heads = q.shape[0], q.shape[1]
+    (pages, kv_heads, page_size, dim), index = _caches(k_cache, v_cache, False)
+    shape, qs = _rows(q, "q", index, None, None, dim)
+    T, heads, _ = shape
     if heads % kv_heads:
         raise ValueError("q heads (%d) must be a multiple of kv heads (%d)" % (heads, kv_heads))
-    _require_ints(ctx_lens, "ctx_lens", dev, (None,))
-    R = ctx_lens.shape[0]
-    _require_ints(block_table, "block_table", dev, (R, None))
-    _require_ints(query_start, "query_start", dev, (R + 1,))
-    words = 0
+    R, _ = _vector(ctx_lens, "ctx_lens", None, index)
+    if R or block_table.dim() != 2:
+        max_pages = _matrix(block_table, "block_table", R, index)
+    else:
+        max_pages = max(block_table.shape[1], 1)
+    _vector(query_start, "query_start", R + 1, index)
+    words, mask_ptr = 0, None
     if mask is not None:
-        _require_ints(mask, "mask", dev, (T, None), torch.int64)
-        words = mask.shape[1]
-        if words == 0:
-            raise ValueError("mask must have at least one word a token")
-    out = _out_tensor(out, (T, heads, dim), dev, "out")
-    with _OnDevice(dev):
-        need = lib.swiglu_tree_attention_workspace_bytes(T, heads, kv_heads, dim)
-        ws_ptr, ws_bytes = None, 0
-        if need:
-            if workspace is None:
-                workspace = _workspace(dev, need, stream)
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _check(lib.swiglu_tree_attention(
-            q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
-            block_table.data_ptr(), R, block_table.shape[1], ctx_lens.data_ptr(),
-            query_start.data_ptr(), None if mask is None else mask.data_ptr(), words,
-            dim ** -0.5 if scale is None else float(scale), out.data_ptr(), T, heads, kv_heads,
-            dim, ws_ptr, ws_bytes, _stream_handle(stream)), "swiglu_tree_attention")
+        words = _matrix(mask, "mask", T, index, _I64)
+        mask_ptr = mask.data_ptr()
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    elif (not isinstance(out, torch.Tensor) or not out.is_cuda or out.dtype is not _BF16
+          or out.shape != shape or not out.is_contiguous() or out.get_device() != index):
+        _refuse(out, "out", index, _BF16, list(shape))
+    key = (index, T, heads, kv_heads, dim)
+    need = _ws_bytes.get(key)
+    if need is None:
+        with torch.cuda.device(index):
+            need = _ws_bytes[key] = swiglu_tree_attention_workspace_bytes(T, heads, kv_heads, dim)
+    ws_ptr, ws_bytes = None, 0
+    if need:
+        if workspace is None:
+            workspace = _workspace(index, need, stream)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call("swiglu_tree_attention", load_library().swiglu_tree_attention, index, stream,
+          q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
+          block_table.data_ptr(), R, max_pages, ctx_lens.data_ptr(), query_start.data_ptr(),
+          mask_ptr, words, dim ** -0.5 if scale is None else float(scale), out.data_ptr(), T,
+          heads, kv_heads, dim, ws_ptr, ws_bytes)
     return out
 
 
@@ -244,21 +268,16 @@ def swiglu_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tabl
     among the request's new tokens, path_lens [R] of them) behind the context,
     in the caches of one layer or of all ([layers, ...]); returns the new
     context lengths."""
-    lib = load_library()
-    shape = _require_caches(k_cache, v_cache, True)
+    shape, index = _caches(k_cache, v_cache, True)
     layers = shape[0] if len(shape) == 5 else 1
     pages, heads, page_size, dim = shape[-4:]
-    dev = k_cache.device
-    _require_ints(ctx_lens, "ctx_lens", dev, (None,))
-    R = ctx_lens.shape[0]
-    _require_ints(block_table, "block_table", dev, (R, None))
-    _require_ints(paths, "paths", dev, (R, None))
-    _require_ints(path_lens, "path_lens", dev, (R,))
+    R, _ = _vector(ctx_lens, "ctx_lens", None, index)
+    max_pages = _matrix(block_table, "block_table", R, index)
+    width = _matrix(paths, "paths", R, index)
+    _vector(path_lens, "path_lens", R, index)
     new_ctx = torch.empty_like(ctx_lens)
-    with _OnDevice(dev):
-        _check(lib.swiglu_cache_accept(
-            k_cache.data_ptr(), v_cache.data_ptr(), layers, pages, heads, page_size, dim,
-            block_table.data_ptr(), R, block_table.shape[1], ctx_lens.data_ptr(),
-            paths.data_ptr(), paths.shape[1], path_lens.data_ptr(), new_ctx.data_ptr(),
-            _stream_handle(stream)), "swiglu_cache_accept")
+    _call("swiglu_cache_accept", load_library().swiglu_cache_accept, index, stream,
+          k_cache.data_ptr(), v_cache.data_ptr(), layers, pages, heads, page_size, dim,
+          block_table.data_ptr(), R, max_pages, ctx_lens.data_ptr(), paths.data_ptr(), width,
+          path_lens.data_ptr(), new_ctx.data_ptr())
     return new_ctx
