@@ -427,13 +427,27 @@ __device__ __forceinline__ uint2 tree_produce(const CUtensorMap &tmQ, const CUte
     return make_uint2(issued, parity);
 }
 
-// ---- MMA issuer: one thread
+// ---- MMA issuer: one thread. It is on every tile's critical path, so unlike
+// the other roles it keeps what it follows in registers.
+struct TreeIssue {   // of an entry
+    int kind, steps, tiles[2], edge[2], tail[2];
+    __device__ __forceinline__ void read(const TreeEntry &e) {
+        kind = e.kind;
+        steps = e.steps;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            tiles[s] = steps ? e.tiles[s] : 0;   // (the last entry has only its steps)
+            edge[s] = e.edge[s];
+            tail[s] = e.tail[s];
+        }
+    }
+};
 template <int D, bool NARROW>
 __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
     using C = TreeCfg<D, NARROW>;
     const TreeBars<D> bars{smem_u32(blk.smem)};
     volatile int *abort_flag = tree_abort<D>(blk.smem);
-    TreeCursor<D, NARROW> k{bars, tree_entries<D>(blk.smem), abort_flag};
+    const TreeEntry *entries = tree_entries<D>(blk.smem);
     // the scores: 128 rows x 128 positions, or 128 positions x 32 rows
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, NARROW ? kTreeNarrow : kTreeTile);
     // the result: 128 rows x D, V as it lies; or D x 32 rows, both as they lie
@@ -443,100 +457,109 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
     // narrow: the weights' sums, as a product with a block of ones, so that they
     // need no registers during the tiles and no exchange between threads
     constexpr uint32_t idesc_l = idesc_bf16_f32(128, kTreeNarrow) | kIdescBMnMajor;
-    // the next entry's first Q tile, the stages of the K and V tiles in use
-    int qb = 0, kstage = 0, vstage = 0;
-    uint32_t qphase = 0, pphase = 0, fphase = 0;
-    bool ok = k.start();
-    while (ok && (k.cur || k.nxt->steps)) {
-#pragma unroll 1
-        for (int op = 0; op < 4; ++op) {
-            const bool is_k = op & 1;
-            const int s = op >> 1, step = is_k ? k.nstep : k.step;
-            const TreeEntry *e = is_k ? k.nxt : k.cur;
-            if (!e || step >= e->steps) continue;
-            const TreePart &x = e->part[s];
-            if (!x.active(step)) continue;
-            const int tile = x.tile(step);
-            const bool own = e->own_kv(step, s);
-            const bool last_use = s == 1 || e->kind != kTreePair;   // of the K or V tile
-            if (is_k) {
-                const int buf = e->two_q() ? qb ^ s : qb;
-                if (step == 0 && (s == 0 || e->two_q())) {
-                    ok = tree_wait(bars.q_full(buf), (qphase >> buf) & 1u, abort_flag);
-                    if (!ok) break;
-                    qphase ^= 1u << buf;
-                }
-                if (own) {
-                    ok = tree_wait(bars.kv_full(k.stage), k.phase, abort_flag);
-                    if (!ok) break;
-                    kstage = k.stage;
-                    k.advance();
-                }
-                tc_fence_after();
-                const uint64_t kd =
-                    smem_desc(bars.base + C::OFF_KV + kstage * C::TILE, 16, C::GROUP);
-                const uint64_t qd = smem_desc(bars.base + C::OFF_Q + buf * C::QBUF, 16, 1024);
-                const uint32_t acc = blk.tmem + 128 * s;
+    TreeIssue cur{}, nxt{};   // cur.steps = 0 before the first entry
+    int step = 0, nstep = 0, seq = 0;
+    // the ring; the stages of the K and V tiles in use; nxt's first Q tile
+    int stage = 0, kstage = 0, vstage = 0, qb = 0;
+    uint32_t phase = 0, qphase = 0, pphase = 0, fphase = 0;
+    auto next_stage = [&](int &at) {   // the ring's next tile, once it is there
+        if (!tree_wait(bars.kv_full(stage), phase, abort_flag)) return false;
+        at = stage;
+        if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        return true;
+    };
+    auto fetch = [&] {
+        const int i = seq % kTreeEntries;
+        nstep = 0;
+        if (!tree_wait(bars.e_full(i), (seq / kTreeEntries) & 1, abort_flag)) return false;
+        nxt.read(entries[i]);
+        return true;
+    };
+    bool ok = fetch();
+    while (ok) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t ko = kd + (i >> 2) * (1024 >> 4) + 2u * (i & 3);
-                    const uint64_t qo = qd + (i >> 2) * (C::Q_HALF >> 4) + 2u * (i & 3);
-                    umma_bf16(acc, NARROW ? ko : qo, NARROW ? qo : ko, idesc_s, i != 0);
-                }
-                umma_commit(bars.s_full(s));
-                if (last_use) umma_commit(bars.kv_empty(kstage));
-                // the last scores that need this Q tile
-                if (tile + 1 == x.end) {
-                    umma_commit(bars.q_empty(buf));
-                    if (!e->two_q()) qb ^= 1;
-                }
-            } else {
-                if (own) {
-                    ok = tree_wait(bars.kv_full(k.stage), k.phase, abort_flag);
-                    if (!ok) break;
-                    vstage = k.stage;
-                    k.advance();
-                    if (x.edge(tile)) {
+        for (int s = 0; s < 2; ++s) {
+            if (!ok) break;
+            if (step < cur.tiles[s]) {   // the result's product
+                if (s == 0 || cur.kind != kTreePair) {
+                    ok = next_stage(vstage);
+                    if (ok && step >= cur.edge[s]) {
                         ok = tree_wait(bars.v_fixed(vstage), (fphase >> vstage) & 1u, abort_flag);
-                        if (!ok) break;
                         fphase ^= 1u << vstage;
                     }
                 }
-                ok = tree_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
+                ok = ok && tree_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
                 if (!ok) break;
                 pphase ^= 1u << s;
                 tc_fence_after();
-                // positions of the tile, in 16s (the rest has no weight)
-                const int count = tree_min(8, (x.len - tile * kTreeTile + 15) >> 4);
                 const uint64_t vd = smem_desc(bars.base + C::OFF_KV + vstage * C::TILE,
                                               D == 128 ? 1024 : 0, C::GROUP);
                 const uint32_t acc = blk.tmem + TreeShared<D>::TMEM_O + D * s;
                 constexpr uint32_t kstep = 2 * C::GROUP >> 4;   // 16 positions of V
                 const uint32_t more = step != 0;
-                if constexpr (NARROW) {
-                    const uint64_t wd =
-                        smem_desc(bars.base + C::OFF_W + s * C::W_BYTES, 16, 512, 4);
+                const bool last = step + 1 == cur.tiles[s];
+                // positions of the tile, in 16s (the rest has no weight)
+                const int count = last ? cur.tail[s] : kTreeTile / 16;
 #pragma unroll
-                    for (int i = 0; i < kTreeTile / 16; ++i) {
-                        if (i >= count) break;
+                for (int i = 0; i < kTreeTile / 16; ++i) {
+                    if (i >= count) break;
+                    if constexpr (NARROW) {
+                        const uint64_t wd =
+                            smem_desc(bars.base + C::OFF_W + s * C::W_BYTES, 16, 512, 4);
                         umma_bf16(acc, vd + kstep * i, wd + 64u * i, idesc_o, more || i != 0);
                         umma_bf16_ts(acc + 32, blk.tmem + TreeShared<D>::TMEM_ONES, wd + 64u * i,
                                      idesc_l, more || i != 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kTreeTile / 16; ++i) {
-                        if (i >= count) break;
+                    } else {
                         umma_bf16_ts(acc, blk.tmem + 128 * s + 64 * (i >> 2) + 8 * (i & 3),
                                      vd + kstep * i, idesc_o, more || i != 0);
                     }
                 }
-                if (last_use) umma_commit(bars.kv_empty(vstage));
-                if (tile + x.stride >= x.end) umma_commit(bars.o_full(s));
+                if (s == 1 || cur.kind != kTreePair) umma_commit(bars.kv_empty(vstage));
+                if (last) umma_commit(bars.o_full(s));
+            }
+            if (nstep < nxt.tiles[s]) {   // the next scores
+                const bool two_q = nxt.kind != kTreeSplit;
+                const int buf = two_q ? qb ^ s : qb;
+                if (nstep == 0 && (s == 0 || two_q)) {
+                    ok = tree_wait(bars.q_full(buf), (qphase >> buf) & 1u, abort_flag);
+                    qphase ^= 1u << buf;
+                }
+                if (s == 0 || nxt.kind != kTreePair) ok = ok && next_stage(kstage);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t kd =
+                    smem_desc(bars.base + C::OFF_KV + kstage * C::TILE, 16, C::GROUP);
+                const uint64_t qd = smem_desc(bars.base + C::OFF_Q + buf * C::QBUF, 16, 1024);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t ko = kd + (i >> 2) * (1024 >> 4) + 2u * (i & 3);
+                    const uint64_t qo = qd + (i >> 2) * (C::Q_HALF >> 4) + 2u * (i & 3);
+                    umma_bf16(blk.tmem + 128 * s, NARROW ? ko : qo, NARROW ? qo : ko, idesc_s,
+                              i != 0);
+                }
+                umma_commit(bars.s_full(s));
+                if (s == 1 || nxt.kind != kTreePair) umma_commit(bars.kv_empty(kstage));
+                // the last scores that need this Q tile: the part's, in a split
+                // those of the entry's last tile
+                const bool last = nstep + 1 == nxt.tiles[s];
+                if (two_q ? last : nstep + 1 == nxt.steps && (s == 1 || nstep >= nxt.tiles[1]))
+                    umma_commit(bars.q_empty(buf));
             }
         }
-        if (ok && k.nxt->steps == 0) break;
-        if (ok) ok = k.move(true);
+        if (!ok || nxt.steps == 0) break;
+        if (nstep == 0) {   // into the next entry
+            if (seq > 0) mbar_arrive(bars.e_empty((seq - 1) % kTreeEntries));
+            cur = nxt;
+        }
+        step = nstep++;
+        if (nstep == cur.steps) {
+            if (cur.kind == kTreeSplit) qb ^= 1;
+            ++seq;
+            ok = fetch();
+        }
     }
     if (!ok) tree_give_up(abort_flag, kStatusMmaTimeout);
 }
@@ -974,29 +997,36 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
 #pragma unroll 1
             for (int i = 32; row_on && i >= 0; i -= 32) see = see << 32 | tree_visible(t, x0 + i);
         }
-        auto scores = [&](int i, uint32_t (&v)[32]) {
-            tmem_ld_32x32b_x32(ts + 64 * half + 32 * i, v);
+        // 16 scores at a time, the next ones on their way from TMEM meanwhile
+        const uint32_t tv = ts + 64 * half;
+        auto arrived = [&](int i, uint32_t (&v)[16]) {
             tmem_ld_wait();
-            reg_fence32(v);
-            const uint32_t bits = static_cast<uint32_t>(see >> (32 * i));
-            if (bits != ~0u) {
+            reg_fence16(v);
+            const uint32_t bits = static_cast<uint32_t>(see >> (16 * i)) & 0xFFFFu;
+            if (bits != 0xFFFFu) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 16; ++j)
                     if (!((bits >> j) & 1u)) v[j] = 0xFF800000u;
             }
         };
         float top = -INFINITY;
         if (warp_on) {
+            uint32_t v[2][16];
+            tmem_ld_32x32b_x16(tv, v[0]);
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                uint32_t v[32];
-                scores(i, v);
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 2)
-                    mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3], fmaxf(__uint_as_float(v[j]),
-                                                                     __uint_as_float(v[j + 1])));
-                top = fmaxf(fmaxf(top, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
+                for (int u = 0; u < 2; ++u) {
+                    arrived(i + u, v[u]);
+                    if (i + u < 3) tmem_ld_32x32b_x16(tv + 16 * (i + u + 1), v[u ^ 1]);
+                    float mx[2] = {top, -INFINITY};
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2)
+                        mx[(j >> 1) & 1] = fmaxf(mx[(j >> 1) & 1],
+                                                 fmaxf(__uint_as_float(v[u][j]),
+                                                       __uint_as_float(v[u][j + 1])));
+                    top = fmaxf(mx[0], mx[1]);
+                }
             }
         }
         const bool rise = fresh || (row_on && top * sc > m * sc + kTreeRescale);
@@ -1031,21 +1061,28 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
             // no maximum so far: weights 2^(-inf - 0) = 0
             const float base = m == -INFINITY ? 0.f : -m * sc;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t v[2][16];
+            tmem_ld_32x32b_x16(tv, v[0]);
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                uint32_t v[32], p[16];
-                scores(i, v);
+            for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float lo, hi;
-                    fma2(lo, hi, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), sc, base);
-                    lo = ex2(lo);
-                    hi = ex2(hi);
-                    add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
-                    p[j] = pack_bf16x2(lo, hi);
+                for (int u = 0; u < 2; ++u) {
+                    arrived(i + u, v[u]);
+                    if (i + u < 3) tmem_ld_32x32b_x16(tv + 16 * (i + u + 1), v[u ^ 1]);
+                    uint32_t p[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float lo, hi;
+                        fma2(lo, hi, __uint_as_float(v[u][2 * j]), __uint_as_float(v[u][2 * j + 1]),
+                             sc, base);
+                        lo = ex2(lo);
+                        hi = ex2(hi);
+                        add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
+                        p[j] = pack_bf16x2(lo, hi);
+                    }
+                    // over this half's own scores, those read already
+                    tmem_st_32x32b_x8(tv + 8 * (i + u), p);
                 }
-                // over this half's own scores, those read already
-                tmem_st_32x32b_x16(ts + 64 * half + 16 * i, p);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_st_wait();

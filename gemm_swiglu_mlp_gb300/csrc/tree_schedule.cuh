@@ -188,6 +188,9 @@ struct TreeEntry {
     TreePart part[2];
     int kind;
     int steps;        // 0: nothing left
+    // for the MMA issuer, each part: its tiles, the first of them that needs a
+    // look, and how many 16s of positions the last one has
+    int tiles[2], edge[2], tail[2];
     SWIGLU_HD bool two_q() const { return kind != kTreeSplit; }    // a Q tile a group
     // group s has a K and a V tile of its own in a step
     SWIGLU_HD bool own_kv(int step, int s) const {
@@ -290,6 +293,16 @@ struct TreeWalk {
             }
         }
         e->part[1] = p;
+        for (int k = 0; k < 2; ++k) {
+            const TreePart &x = e->part[k];
+            // (strides are 1 or 2)
+            const int n = tree_max((x.end - x.first + x.stride - 1) >> (x.stride - 1), 0);
+            const int clear = x.edge_from / kTreeTile - x.first;   // tiles before the first edge
+            e->tiles[k] = n;
+            e->edge[k] = tree_max((clear + x.stride - 1) >> (x.stride - 1), 0);
+            e->tail[k] = tree_min(
+                (x.len - (x.first + (n - 1) * x.stride) * kTreeTile + 15) >> 4, kTreeTile / 16);
+        }
     }
 };
 

@@ -134,6 +134,17 @@ int main(int argc, char **argv) {
                     CHECK(e.part[k].used() == !seen[k].empty());
                     units += e.kind == kTreePair && k ? 0 : static_cast<int>(seen[k].size());
                 }
+                // what the MMA issuer goes by
+                for (int k = 0; k < 2; ++k) {
+                    const TreePart &p = e.part[k];
+                    CHECK(e.tiles[k] == static_cast<int>(seen[k].size()));
+                    for (int st = 0; st < e.tiles[k]; ++st) {
+                        CHECK((st >= e.edge[k]) == p.edge(p.tile(st)));
+                        const int rest = p.len - p.tile(st) * kTreeTile;
+                        const int count = rest >= kTreeTile ? 8 : (rest + 15) / 16;
+                        CHECK((st + 1 == e.tiles[k] ? e.tail[k] : 8) == count);
+                    }
+                }
                 CHECK(e.part[0].used() && (e.kind == kTreeSplit || e.part[1].used()));
                 if (e.kind == kTreeSplit)
                     CHECK(static_cast<int>(seen[0].size() + seen[1].size()) == at.te - at.tb);
