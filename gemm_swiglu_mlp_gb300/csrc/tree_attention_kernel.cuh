@@ -365,6 +365,8 @@ __device__ __forceinline__ uint2 tree_produce(const CUtensorMap &tmQ, const CUte
     int qb = 0;
     uint32_t qphase = 0;
     const int pages = kTreeTile >> a.page_shift;   // pages a tile, <= 8
+    // this lane's page: of each group's tile in use, and of its next one
+    int rows0 = 0, rows1 = 0, ahead0 = 0, ahead1 = 0;
     bool ok = __all_sync(~0u, k.start());
     while (ok && (k.cur || k.nxt->steps)) {
 #pragma unroll 1
@@ -397,13 +399,28 @@ __device__ __forceinline__ uint2 tree_produce(const CUtensorMap &tmQ, const CUte
             // the tile's pages up to the item's end
             const int count = tree_min(
                 pages, (x.len - tile * kTreeTile + (1 << a.page_shift) - 1) >> a.page_shift);
-            int row = 0;
-            if (lane < count) {
-                const int page = a.table[x.r * a.max_pages +
-                                         static_cast<long long>(tile) * pages + lane];
+            // a tile's V comes from its K's pages; the next K's are asked for
+            // one step ahead (a load of the table takes as long as a tile)
+            int row = s ? rows1 : rows0;
+            if (is_k) {
+                const int *table = a.table + x.r * a.max_pages +
+                                   static_cast<long long>(tile) * pages + lane;
+                int page = s ? ahead1 : ahead0, next = 0;
+                if (step == 0 && lane < count) page = *table;
+                const int after = tile + x.stride;
+                if (after < x.end &&
+                    (after * pages + lane) << a.page_shift < x.len)
+                    next = table[static_cast<long long>(x.stride) * pages];
                 // outside the cache: a box past its end, filled with zeros
                 row = page >= 0 && page < a.num_pages ? page * g.kv_heads + x.h
                                                       : a.num_pages * g.kv_heads;
+                if (s) {
+                    ahead1 = next;
+                    rows1 = row;
+                } else {
+                    ahead0 = next;
+                    rows0 = row;
+                }
             }
             ok = warp_wait(bars.kv_empty(k.stage), k.phase ^ 1u, abort_flag);
             if (!ok) break;
