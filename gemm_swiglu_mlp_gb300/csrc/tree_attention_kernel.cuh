@@ -530,7 +530,7 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                         umma_bf16_ts(acc + 32, blk.tmem + TreeShared<D>::TMEM_ONES, wd + 64u * i,
                                      idesc_l, more || i != 0);
                     } else {
-                        umma_bf16_ts(acc, blk.tmem + 128 * s + 64 * (i >> 2) + 8 * (i & 3),
+                        umma_bf16_ts(acc, blk.tmem + 128 * s + 64 * (i >> 2) + 32 + 8 * (i & 3),
                                      vd + kstep * i, idesc_o, more || i != 0);
                     }
                 }
@@ -1004,46 +1004,41 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
         ph.scores ^= 1u;
         tc_fence_after();
         const bool fresh = tile == x.first;
-        // the 64 scores, 32 at a time, twice: first their maximum, then the
-        // weights (kept meanwhile they would be most of a thread's registers)
-        const int x0 = tile * kTreeTile + 64 * half;
-        unsigned long long see = ~0ull;   // bit j: position x0 + j is seen
+        // The 64 scores, 32 at a time: first their maximum, then the weights, the
+        // second 32 from the registers that they are still in, the first 32 read
+        // again (all 64 kept would be most of a thread's registers).
+        const uint32_t tv = ts + 64 * half;
+        unsigned long long see = ~0ull;   // bit j: this half's position j is seen
         if (x.edge(tile)) {
             const TreeSight t = sight();
             see = 0;
 #pragma unroll 1
-            for (int i = 32; row_on && i >= 0; i -= 32) see = see << 32 | tree_visible(t, x0 + i);
+            for (int i = 32; row_on && i >= 0; i -= 32)
+                see = see << 32 | tree_visible(t, tile * kTreeTile + 64 * half + i);
         }
-        // 16 scores at a time, the next ones on their way from TMEM meanwhile
-        const uint32_t tv = ts + 64 * half;
-        auto arrived = [&](int i, uint32_t (&v)[16]) {
+        uint32_t v[32];
+        auto scores = [&](int i) {
+            tmem_ld_32x32b_x32(tv + 32 * i, v);
             tmem_ld_wait();
-            reg_fence16(v);
-            const uint32_t bits = static_cast<uint32_t>(see >> (16 * i)) & 0xFFFFu;
-            if (bits != 0xFFFFu) {
+            reg_fence32(v);
+            const uint32_t bits = static_cast<uint32_t>(see >> (32 * i));
+            if (bits != ~0u) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 32; ++j)
                     if (!((bits >> j) & 1u)) v[j] = 0xFF800000u;
             }
         };
         float top = -INFINITY;
         if (warp_on) {
-            uint32_t v[2][16];
-            tmem_ld_32x32b_x16(tv, v[0]);
 #pragma unroll 1
-            for (int i = 0; i < 4; i += 2) {
+            for (int i = 0; i < 2; ++i) {
+                scores(i);
+                float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    arrived(i + u, v[u]);
-                    if (i + u < 3) tmem_ld_32x32b_x16(tv + 16 * (i + u + 1), v[u ^ 1]);
-                    float mx[2] = {top, -INFINITY};
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2)
-                        mx[(j >> 1) & 1] = fmaxf(mx[(j >> 1) & 1],
-                                                 fmaxf(__uint_as_float(v[u][j]),
-                                                       __uint_as_float(v[u][j + 1])));
-                    top = fmaxf(mx[0], mx[1]);
-                }
+                for (int j = 0; j < 32; j += 2)
+                    mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3],
+                                             fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+                top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             }
         }
         const bool rise = fresh || (row_on && top * sc > m * sc + kTreeRescale);
@@ -1062,15 +1057,15 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
             }
             if (!fresh && warp_on && __any_sync(~0u, row_on && f != 1.f)) {
 #pragma unroll 1
-                for (int col = half * (D / 2); col < (half + 1) * (D / 2); col += 16) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(to + col, o);
+                for (int col = half * (D / 2); col < (half + 1) * (D / 2); col += 8) {
+                    uint32_t o[8];
+                    tmem_ld_32x32b_x8(to + col, o);
                     tmem_ld_wait();
-                    reg_fence16(o);
+                    reg_fence8(o);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 8; ++j)
                         o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                    tmem_st_32x32b_x16(to + col, o);
+                    tmem_st_32x32b_x8(to + col, o);
                 }
             }
         }
@@ -1078,28 +1073,21 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
             // no maximum so far: weights 2^(-inf - 0) = 0
             const float base = m == -INFINITY ? 0.f : -m * sc;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t v[2][16];
-            tmem_ld_32x32b_x16(tv, v[0]);
 #pragma unroll 1
-            for (int i = 0; i < 4; i += 2) {
+            for (int i = 1; i >= 0; --i) {
+                if (i == 0) scores(0);
+                uint32_t p[16];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    arrived(i + u, v[u]);
-                    if (i + u < 3) tmem_ld_32x32b_x16(tv + 16 * (i + u + 1), v[u ^ 1]);
-                    uint32_t p[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float lo, hi;
-                        fma2(lo, hi, __uint_as_float(v[u][2 * j]), __uint_as_float(v[u][2 * j + 1]),
-                             sc, base);
-                        lo = ex2(lo);
-                        hi = ex2(hi);
-                        add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
-                        p[j] = pack_bf16x2(lo, hi);
-                    }
-                    // over this half's own scores, those read already
-                    tmem_st_32x32b_x8(tv + 8 * (i + u), p);
+                for (int j = 0; j < 16; ++j) {
+                    float lo, hi;
+                    fma2(lo, hi, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), sc, base);
+                    lo = ex2(lo);
+                    hi = ex2(hi);
+                    add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
+                    p[j] = pack_bf16x2(lo, hi);
                 }
+                // over this half's own scores, those that are not needed again
+                tmem_st_32x32b_x16(tv + 32 + 16 * i, p);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_st_wait();
