@@ -4,13 +4,19 @@
 
 One translation unit, one -gencode (compute_103a -> sm_103a), static CUDA
 runtime (the library needs no libcudart/libcuda at load time; the driver is
-reached through cudaGetDriverEntryPointByVersion when a call needs it).
+reached through cudaGetDriverEntryPointByVersion when a call needs it). Beside
+it the binding module of the paged-cache calls, host C++ against the installed
+PyTorch (its version is in the file's name).
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
+import threading
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -18,6 +24,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libswiglu_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+BINDING_SOURCE = os.path.join(CSRC, "cache_binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_cache_binding_%s.so" % "".join(
+    c if c.isalnum() else "_" for c in importlib.metadata.version("torch")))
 SOURCES = [os.path.join(CSRC, "swiglu_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(INCLUDE, "swiglu.h")]
@@ -46,14 +55,63 @@ def build_fault_injection_library(out_path: str) -> str:
     return out_path
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _newer(path: str, deps) -> bool:
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(d) <= t for d in DEPS)
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB_PATH, DEPS)
+
+
+def binding_command(out_path: str):
+    """g++ on the binding module, with the installed PyTorch's headers and libraries."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch_dir, "include")
+    cuda = os.path.dirname(os.path.dirname(nvcc_path())) or "/usr/local/cuda"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + INCLUDE, "-I" + inc,
+            "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
+            "-o", out_path, BINDING_SOURCE, "-L" + os.path.join(torch_dir, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
+def build_binding(force: bool = False) -> str:
+    if not force and _newer(BINDING_PATH, [BINDING_SOURCE, os.path.join(INCLUDE, "swiglu.h")]):
+        return BINDING_PATH
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    proc = subprocess.run(binding_command(tmp), capture_output=True, text=True)
+    if proc.returncode != 0:
+        sys.stderr.write(proc.stdout + proc.stderr)
+        raise RuntimeError("g++ failed building %s" % os.path.basename(BINDING_PATH))
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Both, at the same time; returns the library's path."""
+    errors = []
+
+    def binding():
+        try:
+            build_binding(force)
+        except Exception as e:  # raised below, once the library is there
+            errors.append(e)
+
+    t = threading.Thread(target=binding)
+    t.start()
+    try:
+        path = build_library(force, verbose)
+    finally:
+        t.join()
+    if errors:
+        raise errors[0]
+    return path
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
