@@ -132,10 +132,10 @@ int tree_launch(const CUtensorMap &tmQ, const CUtensorMap &tmQn, const CUtensorM
     cfg.dynamicSmemBytes = TreeShared<D>::SMEM_BYTES;
     cudaError_t err = cudaLaunchKernelEx(&cfg, tree_attention_kernel<D>, tmQ, tmQn, tmK, tmV, a);
     if (err == cudaSuccess) {
-        cfg.gridDim = dim3(static_cast<unsigned>(2 * sms));
+        cfg.gridDim = dim3(static_cast<unsigned>(sms), kJoinBlocks);
         cfg.blockDim = dim3(kJoinThreads);
         cfg.dynamicSmemBytes = 0;
-        err = cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a, sms);
+        err = cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a);
     }
     if (err != cudaSuccess) {
         cudaGetLastError();
@@ -448,7 +448,7 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     uint8_t *base = static_cast<uint8_t *>(workspace);
     a.chains = reinterpret_cast<int4 *>(base);
     a.stats = reinterpret_cast<float2 *>(base + ws.stats);
-    a.partial = reinterpret_cast<float *>(base + ws.partial);
+    a.partial = reinterpret_cast<float4 *>(base + ws.partial);
     a.max_pages = max_pages;
     a.scale_log2 = scale * 1.4426950408889634f;   // log2(e)
     a.q_heads = static_cast<int>(q_heads);

@@ -67,7 +67,7 @@ struct TreeAttnArgs {
     const unsigned long long *mask;    // [tokens][mask_words], or null
     const uint16_t *v_cache;           // [pages][kv heads][page rows][D]
     uint16_t *out;                     // [tokens][q heads][D]
-    float *partial;                    // [2 * grid][part_rows][D]
+    float4 *partial;                   // [2 * grid][D / 4][part_rows], four columns a row
     float2 *stats;                     // [2 * grid][part_rows]: maximum, sum
     int4 *chains;                      // [grid]: items that begin in a block and go on
     long long max_pages;
@@ -893,8 +893,9 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
     tc_fence_after();
     const bool flagged = flags[2 * slot + s] || (split && flags[2 * slot + (s ^ 1)]);
     const bool whole = (x.flags & kPartWhole) != 0;
-    const long long prow =
-        static_cast<long long>(2 * c + ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows;
+    const long long part = 2 * c + ((x.flags & kPartBegins) ? 1 : 0);
+    const long long prow = part * a.part_rows;
+    float4 *const sums = a.partial + part * (D / 4) * a.part_rows;
     const float *m0 = tree_stats<D>(blk.smem) + kMax, *m1 = m0 + 256;
     const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
     // the halves of a group, in a split all four, take the rows in turn
@@ -928,7 +929,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
             a.out[(first_row + static_cast<long long>(t) * a.q_heads + (r - t * g.group)) * D + row] =
                 *reinterpret_cast<const uint16_t *>(&b);
         } else {
-            a.partial[(prow + r) * D + row] = value;
+            reinterpret_cast<float *>(sums + (row >> 2) * a.part_rows + r)[row & 3] = value;
             if (row == 0) a.stats[prow + r] = make_float2(top, sum);
         }
     }
@@ -948,8 +949,9 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
                     a.out + (first_row + static_cast<long long>(t) * a.q_heads + r % g.group) * D + row,
                     1, sight, x0, x1, table, a.page_shift, a.num_pages, g.kv_heads * head_step, vc);
             else
-                tree_add_nonfinite<D>(a.partial + (prow + r) * D + row, 1, sight, x0, x1, table,
-                                      a.page_shift, a.num_pages, g.kv_heads * head_step, vc);
+                tree_add_nonfinite<D>(
+                    reinterpret_cast<float *>(sums + (row >> 2) * a.part_rows + r) + (row & 3), 1,
+                    sight, x0, x1, table, a.page_shift, a.num_pages, g.kv_heads * head_step, vc);
         }
     }
     tc_fence_before();
@@ -1123,10 +1125,9 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
         const bool flagged = flags[2 * slot + s] || (split && flags[2 * slot + (s ^ 1)]);
         const bool whole = (x.flags & kPartWhole) != 0;
         // partial results: slot 2c + 1 for an item that begins here, 2c for others
-        const long long prow =
-            static_cast<long long>(2 * static_cast<int>(blockIdx.x) +
-                                   ((x.flags & kPartBegins) ? 1 : 0)) * a.part_rows +
-            ((x.flags & kPartSecond) ? 128 : 0) + row;
+        const long long part =
+            2 * static_cast<int>(blockIdx.x) + ((x.flags & kPartBegins) ? 1 : 0);
+        const int in_part = ((x.flags & kPartSecond) ? 128 : 0) + row;
         float2 st = stats[row];
         float w0 = 1.f, w1 = 0.f;
         if (split) {
@@ -1138,7 +1139,8 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
             w1 = a1.x == -INFINITY ? 0.f : ex2((a1.x - top) * sc);
             st = make_float2(top, a0.y * w0 + a1.y * w1);
         }
-        if (!whole && row_on && half == 0 && (!split || s == 0)) a.stats[prow] = st;
+        if (!whole && row_on && half == 0 && (!split || s == 0))
+            a.stats[part * a.part_rows + in_part] = st;
         const float inv = whole ? (st.y == 0.f ? 0.f : 1.f / st.y) : 1.f;
         const uint32_t t0 = blk.tmem + lanes + TreeShared<D>::TMEM_O, t1 = t0 + D;
         // this thread's columns: its half of the row, in a split its quarter
@@ -1146,7 +1148,8 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
         const int c0 = (split ? 2 * s + half : half) * width;
         uint16_t *const out = a.out + (static_cast<long long>(x.tok + my_tok) * a.q_heads +
                                        x.h * g.group + (row - my_tok * g.group)) * D;
-        float *const sums = a.partial + prow * D;
+        // (the lanes' rows next to each other)
+        float4 *const sums = a.partial + part * (D / 4) * a.part_rows + in_part;
 #pragma unroll 1
         for (int col = c0; col < c0 + width; col += 16) {
             uint32_t o[16];
@@ -1181,10 +1184,11 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
                     dst[j] = make_uint4(b[0], b[1], b[2], b[3]);
                 }
             } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(sums + col);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    sums[(col / 4 + j) * a.part_rows] =
+                        make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                    __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
             }
         }
         if (flagged && row_on) {
@@ -1197,8 +1201,10 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
                 tree_add_nonfinite<D>(out + c0, width, sight(), x0, x1, table, a.page_shift,
                                       a.num_pages, g.kv_heads * head_step, vc);
             else
-                tree_add_nonfinite<D>(sums + c0, width, sight(), x0, x1, table, a.page_shift,
-                                      a.num_pages, g.kv_heads * head_step, vc);
+                for (int col = 0; col < width; col += 4)
+                    tree_add_nonfinite<D>(
+                        reinterpret_cast<float *>(sums + (c0 + col) / 4 * a.part_rows), 4, sight(),
+                        x0, x1, table, a.page_shift, a.num_pages, g.kv_heads * head_step, vc + col);
         }
     }
     tc_fence_before();
@@ -1446,73 +1452,62 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // ---------------------------------------------------------------- partial results
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 8;   // blocks a chain
 
 // Items that several blocks worked on: out = sum_b w_b o_b / sum_b w_b l_b,
 // w_b = exp(scale * (m_b - max m)), in block order, so that the result does
-// not depend on which block finished first. One warp a row; the rows of all
-// such items are dealt evenly over the grid's warps, each of which adds up
-// the items' row counts for itself.
+// not depend on which block finished first. Blocks (c, 0..) sum the item that
+// begins in block c, if one does; a warp takes 32 rows (a lane each: partial
+// results lie with the rows next to each other) and eight columns.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a, int blocks) {
-    constexpr int V = D / 32;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int warps = static_cast<int>(gridDim.x) * (kJoinThreads / 32);
+    const int c = static_cast<int>(blockIdx.x), lane = threadIdx.x & 31;
+    const int4 chain = a.chains[c];   // last block, first token, head, tokens (0: none)
+    if (chain.w == 0) return;
     const int tpt = a.geom.tpt, group = a.geom.group;
-    // consecutive rows on different SMs
-    int task = (threadIdx.x >> 5) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    for (int chunk = 0; chunk < blocks; chunk += 32) {
-        // items that begin in blocks chunk .. chunk + 31: last block, first
-        // token, head, tokens (0: none)
-        const int4 mine = chunk + lane < blocks ? a.chains[chunk + lane] : make_int4(0, 0, 0, 0);
-        int upto = mine.w * group;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(~0u, upto, d);
-            if (lane >= d) upto += x;
+    const int parts = chain.x - c + 1;
+    const int rows = chain.w * group;
+    const int groups = (rows + 31) / 32;
+    for (int task = static_cast<int>(blockIdx.y) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+         task < groups * (D / 8); task += kJoinBlocks * (kJoinThreads / 32)) {
+        const int col = task / groups * 8, i = (task % groups) * 32 + lane;
+        if (i >= rows) continue;
+        const int tok = i / group, head = i - tok * group;
+        const int second = tok >= tpt;
+        const int row = 128 * second + (tok - second * tpt) * group + head;
+        // part 0 is the slot of an item that begins in c, the others' of one that goes on
+        float top = -INFINITY;
+        for (int b = 0; b < parts; ++b) {
+            const long long slot = b == 0 ? 2 * c + 1 : 2 * (c + b);
+            top = fmaxf(top, a.stats[slot * a.part_rows + row].x);
         }
-        const int rows = __shfl_sync(~0u, upto, 31);
-        for (; task < rows; task += warps) {
-            const int from = __popc(__ballot_sync(~0u, upto <= task));
-            const int c = chunk + from;
-            const int last = __shfl_sync(~0u, mine.x, from), tok0 = __shfl_sync(~0u, mine.y, from);
-            const int h = __shfl_sync(~0u, mine.z, from), tokens = __shfl_sync(~0u, mine.w, from);
-            const int i = task - (__shfl_sync(~0u, upto, from) - tokens * group);
-            const int tok = i / group, head = i - tok * group;
-            const int rt = tok >= tpt;
-            const long long row = 128 * rt + (tok - rt * tpt) * group + head;
-            const int parts = last - c + 1;
-            // part 0 is the slot of an item that begins in c, the others' of one that goes on
-            auto slot = [&](int b) {
-                return static_cast<long long>(b == 0 ? 2 * c + 1 : 2 * (c + b)) * a.part_rows + row;
-            };
-            float top = -INFINITY;
-            for (int b = lane; b < parts; b += 32) top = fmaxf(top, a.stats[slot(b)].x);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            float acc[V] = {}, l = 0.f;
-#pragma unroll 4
-            for (int b = 0; b < parts; ++b) {
-                const float2 st = a.stats[slot(b)];
-                const float f = st.x == -INFINITY ? 0.f : ex2((st.x - top) * a.scale_log2);
-                const float *o = a.partial + slot(b) * D + V * lane;
-                float v[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[e] = o[e];
-                l = fmaf(st.y, f, l);
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], f, acc[e]);
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(
-                a.out +
-                (static_cast<long long>(tok0 + tok) * a.q_heads + h * group + head) * D + V * lane);
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e)
-                dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        float acc[8] = {}, l = 0.f;
+#pragma unroll 2
+        for (int b = 0; b < parts; ++b) {
+            const long long slot = b == 0 ? 2 * c + 1 : 2 * (c + b);
+            const float2 st = a.stats[slot * a.part_rows + row];
+            const float4 *o = a.partial + (slot * (D / 4) + col / 4) * a.part_rows + row;
+            const float4 x = o[0], y = o[a.part_rows];
+            const float f = st.x == -INFINITY ? 0.f : ex2((st.x - top) * a.scale_log2);
+            l = fmaf(st.y, f, l);
+            acc[0] = fmaf(x.x, f, acc[0]);
+            acc[1] = fmaf(x.y, f, acc[1]);
+            acc[2] = fmaf(x.z, f, acc[2]);
+            acc[3] = fmaf(x.w, f, acc[3]);
+            acc[4] = fmaf(y.x, f, acc[4]);
+            acc[5] = fmaf(y.y, f, acc[5]);
+            acc[6] = fmaf(y.z, f, acc[6]);
+            acc[7] = fmaf(y.w, f, acc[7]);
         }
-        task -= rows;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        *reinterpret_cast<uint4 *>(
+            a.out + (static_cast<long long>(chain.y + tok) * a.q_heads + chain.z * group + head) * D +
+            col) = make_uint4(p[0], p[1], p[2], p[3]);
     }
 }
 
