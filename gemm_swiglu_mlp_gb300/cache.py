@@ -73,6 +73,13 @@ def _workspace(index: int, nbytes: int, stream) -> torch.Tensor:
     return ws
 
 
+def _on(stream, f, *args):
+    """f(*args), its results allocated as `stream`'s own: memory of the current
+    stream may still be in use there by work that `stream` does not wait for."""
+    with torch.cuda.stream(stream):
+        return f(*args)
+
+
 class CachePlan(NamedTuple):
     """What swiglu_cache_plan makes; pass it as `out` to reuse its buffers."""
     query_start: torch.Tensor          # [R + 1] int32
@@ -94,6 +101,9 @@ def swiglu_cache_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, pages_held
     step's tokens: slot -1, mask 0). `free_head` [1] (None: 0) is where the
     free list starts; the next step's is counts[2:3]."""
     native = _binding or _native()
+    if out is None and stream is not None:
+        return _on(stream, swiglu_cache_plan, ctx_lens, new_lens, pages_held, block_table,
+                   free_pages, page_size, max_tokens, parents, free_head)
     if out is None:
         if not isinstance(ctx_lens, torch.Tensor):
             raise TypeError("ctx_lens must be a CUDA tensor")
@@ -129,8 +139,12 @@ def swiglu_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     context and the new tokens in its row of `mask` [tokens, words] int64
     (None: those before it, and itself). The step's own keys and values are
     in the cache already (swiglu_cache_write). `scale` None: 1/sqrt(head size)."""
-    return (_binding or _native()).attend(q, k_cache, v_cache, block_table, ctx_lens, query_start,
-                                          mask, scale, out, workspace, stream)
+    attend = (_binding or _native()).attend
+    if out is None and stream is not None:
+        return _on(stream, attend, q, k_cache, v_cache, block_table, ctx_lens, query_start, mask,
+                   scale, out, workspace, None)
+    return attend(q, k_cache, v_cache, block_table, ctx_lens, query_start, mask, scale, out,
+                  workspace, stream)
 
 
 def swiglu_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -140,5 +154,7 @@ def swiglu_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tabl
     among the request's new tokens, path_lens [R] of them) behind the context,
     in the caches of one layer or of all ([layers, ...]); returns the new
     context lengths."""
-    return (_binding or _native()).accept(k_cache, v_cache, block_table, ctx_lens, paths, path_lens,
-                                          stream)
+    accept = (_binding or _native()).accept
+    if stream is not None:
+        return _on(stream, accept, k_cache, v_cache, block_table, ctx_lens, paths, path_lens, None)
+    return accept(k_cache, v_cache, block_table, ctx_lens, paths, path_lens, None)

@@ -363,6 +363,37 @@ def test_attention_strides_out_and_workspace(sg):
     assert np.array_equal(c.run(sg, q=by_head, workspace=ws), got)     # and bit for bit again
 
 
+def test_results_belong_to_the_given_stream(sg):
+    """A block that the current stream has freed, but still reads, is not handed
+    to a result that another stream writes at once."""
+    ctx = torch.full((64,), 5, dtype=torch.int32, device="cuda")
+    table = torch.zeros(64, 1, dtype=torch.int32, device="cuda")
+    k, v = torch.zeros(2, 1, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    paths = torch.zeros(64, 1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(64, dtype=torch.int32, device="cuda")
+    q = torch.zeros(64, 1, 64, dtype=torch.bfloat16, device="cuda")
+    start = torch.arange(65, dtype=torch.int32, device="cuda")
+    free = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    calls = [lambda: sg.swiglu_cache_accept(k, v, table, ctx, paths, lens, stream=side),
+             lambda: sg.swiglu_tree_attention(q, k, v, table, ctx, start, stream=side),
+             lambda: sg.swiglu_cache_plan(ctx, lens, torch.ones_like(ctx), table, free, 16, 64,
+                                          stream=side).slots]
+    for call in calls:
+        got = call()
+        size = (got.numel(), got.dtype)
+        side.synchronize()
+        del got
+        old = torch.empty(size[0], dtype=size[1], device="cuda")   # of the current stream
+        where = old.data_ptr()
+        del old
+        assert call().data_ptr() != where
+        side.synchronize()
+
+
+
 def test_attention_other_stream_and_graph(sg):
     """Calls on a side stream, and a captured step replayed with other lengths."""
     c = Case(16, [700, 30, 2000], [9, 1, 12], 7, 1, 128, 16, True)
