@@ -479,8 +479,8 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
     // the ring; the stages of the K and V tiles in use; nxt's first Q tile
     int stage = 0, kstage = 0, vstage = 0, qb = 0;
     uint32_t phase = 0, qphase = 0, pphase = 0, fphase = 0;
-    auto next_stage = [&](int &at) {   // the ring's next tile, once it is there
-        if (!tree_wait(bars.kv_full(stage), phase, abort_flag)) return false;
+    auto next_stage = [&](int &at, bool there = false) {   // the ring's next tile, once it is there
+        if (!there && !tree_wait(bars.kv_full(stage), phase, abort_flag)) return false;
         at = stage;
         if (++stage == C::STAGES) {
             stage = 0;
@@ -500,6 +500,7 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if (!ok) break;
+            bool k_there = false;
             if (step < cur.tiles[s]) {   // the result's product
                 if (s == 0 || cur.kind != kTreePair) {
                     ok = next_stage(vstage);
@@ -508,6 +509,8 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                         fphase ^= 1u << vstage;
                     }
                 }
+                // while the weights are due, whether what comes after is there
+                k_there = mbar_test_wait(bars.kv_full(stage), phase);
                 ok = ok && tree_wait(bars.p_ready(s), (pphase >> s) & 1u, abort_flag);
                 if (!ok) break;
                 pphase ^= 1u << s;
@@ -544,7 +547,7 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                     ok = tree_wait(bars.q_full(buf), (qphase >> buf) & 1u, abort_flag);
                     qphase ^= 1u << buf;
                 }
-                if (s == 0 || nxt.kind != kTreePair) ok = ok && next_stage(kstage);
+                if (s == 0 || nxt.kind != kTreePair) ok = ok && next_stage(kstage, k_there);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t kd =
