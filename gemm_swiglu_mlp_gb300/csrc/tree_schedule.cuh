@@ -179,11 +179,22 @@ struct TreePart {
 
 // What both groups do next. kTreeSplit: an item of one row tile, the groups
 // take its even and odd tiles and merge their results. kTreePair: an item of
-// two row tiles, one a group, over the same tiles. kTreeDuo: two short items
-// of one row tile each, one a group; while one group's softmax or result runs,
-// the tensor cores work for the other.
+// two row tiles, one a group, over the same tiles. kTreeDuo: two items of one
+// row tile each, one a group; while one group's softmax or result runs, the
+// tensor cores work for the other.
 enum : int { kTreeSplit = 0, kTreePair = 1, kTreeDuo = 2 };
+// Whether two items with this many tiles make a Duo. It saves both results'
+// merging and the groups never wait for each other, but the group with fewer
+// tiles has nothing to do at the end: so where that is no more than a quarter
+// of the longer one, or a few tiles. Measured (us, with / without): 304 requests
+// of 9 tokens, 7 heads a kv head, contexts of 100 21 / 29, of 900 69 / 73, of
+// 6000 315 / 340; 608 requests of one token, contexts of 100 25 / 33, of 1500
+// 158 / 158.
 constexpr int kTreeDuoTiles = 4;
+SWIGLU_HD bool tree_duo(int a, int b) {
+    const int more = tree_max(a, b);
+    return more <= kTreeDuoTiles || 4 * (more - tree_min(a, b)) <= more;
+}
 struct TreeEntry {
     TreePart part[2];
     int kind;
@@ -281,7 +292,7 @@ struct TreeWalk {
         }
         next(g, load);
         if (!two) {
-            if (mine <= kTreeDuoTiles && left > 0 && !pair(g) && te - tb <= kTreeDuoTiles) {
+            if (left > 0 && !pair(g) && tree_duo(mine, te - tb)) {
                 e->kind = kTreeDuo;
                 e->steps = tree_max(mine, te - tb);
                 p = part(g);
