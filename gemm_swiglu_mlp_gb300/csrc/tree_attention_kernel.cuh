@@ -1315,6 +1315,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     TreeStart *start = reinterpret_cast<TreeStart *>(smem + S::OFF_MISC + 48);
     // the prologue's sums, in the statistics' place
     int2 *warp_sums = reinterpret_cast<int2 *>(tree_stats<D>(smem));
+    float *warp_costs = reinterpret_cast<float *>(warp_sums + 32);
 
     if (warp == 16 && lane == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
@@ -1362,11 +1363,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int r1 = tree_min(r0 + per, g.requests);
     TreeReq q{};
     int mine[2] = {0, 0};   // units: wide, narrow
+    float cost = 0.f;       // of the wide ones
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
         q = load(r);
-        const int u = g.kv_heads * tree_head_units(g, q);
-        if (tree_is_narrow(g, q)) mine[1] += u; else mine[0] += u;
+        const int per_head = tree_head_units(g, q);
+        if (tree_is_narrow(g, q)) {
+            mine[1] += g.kv_heads * per_head;
+        } else {
+            mine[0] += g.kv_heads * per_head;
+            if (per_head) cost += g.kv_heads * tree_wide_cost(g, q, per_head);
+        }
     }
     // sums up to this thread, in its warp and then over the warps
     int upto[2] = {mine[0], mine[1]};
@@ -1374,6 +1381,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
             const int x = __shfl_up_sync(~0u, v[0], d), y = __shfl_up_sync(~0u, v[1], d);
+            cost += __shfl_xor_sync(~0u, cost, d);
             if (lane >= d) {
                 v[0] += x;
                 v[1] += y;
@@ -1382,11 +1390,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
     int sums[2] = {0, 0};
     warp_scan(upto);
-    if (lane == 31) warp_sums[warp] = make_int2(upto[0], upto[1]);
+    if (lane == 31) {
+        warp_sums[warp] = make_int2(upto[0], upto[1]);
+        warp_costs[warp] = cost;
+    }
     __syncthreads();
+    cost = 0.f;
     if (lane < kTreeThreads / 32) {
         sums[0] = warp_sums[lane].x;
         sums[1] = warp_sums[lane].y;
+        cost = warp_costs[lane];
     }
     warp_scan(sums);
     const int before_w = __shfl_sync(~0u, sums[0], (warp - 1) & 31);
@@ -1397,7 +1410,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     blk.smem = smem;
     const int c = static_cast<int>(blockIdx.x);
     const int blocks = tree_min(static_cast<int>(gridDim.x), wide + narrow);
-    const int nb = tree_min(tree_narrow_blocks(narrow, wide, blocks), narrow);
+    const int nb = tree_min(tree_narrow_blocks(narrow, wide, cost, blocks), narrow);
     const int wb = tree_min(blocks - nb, wide);
     const bool is_narrow = c < nb;
     blk.base = is_narrow ? 0 : nb;

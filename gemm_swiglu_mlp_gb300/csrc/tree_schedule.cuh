@@ -96,16 +96,27 @@ SWIGLU_HD_CALL int tree_head_units(const TreeGeom &g, const TreeReq &q) {
     return u;
 }
 
+// What a kv head's `units` cost in the wide form, in quarters of a narrow tile
+// (whose time is its bytes'): a tile of an item of one row tile kTreeOneCost,
+// of two kTreePairCost, as their products and weights take more than the
+// bytes. Measured with half of 64 requests at one token and the others at n, 7
+// heads a kv head, contexts of 4000 (us): all at 4 / 5 / 6 / 8, n = 6
+// 121 / 118 / 133 / 144, n = 36 (one item of two row tiles) 177 / 163 / 157 / 165.
+constexpr int kTreeOneCost = 5, kTreePairCost = 7;
+SWIGLU_HD float tree_wide_cost(const TreeGeom &g, const TreeReq &q, int units) {
+    const int items = tree_items(g, q);
+    float cost = static_cast<float>(units) * kTreePairCost;
+    if (q.n - (items - 1) * 2 * g.tpt <= g.tpt)   // the last item has one row tile
+        cost -= static_cast<float>(tree_item_tiles(g, q, items - 1)) * (kTreePairCost - kTreeOneCost);
+    return cost;
+}
 // How many of `blocks` (>= 2 where both lines have work) blocks take the narrow
-// form's line: in proportion to the units, a wide tile counted as
-// kTreeWideCost / 4 narrow ones (a narrow tile's time is its bytes', a wide
-// one's also its products').
-constexpr int kTreeWideCost = 6;
-SWIGLU_HD int tree_narrow_blocks(int narrow, int wide, int blocks) {
+// form's line: as its share of the cost.
+SWIGLU_HD int tree_narrow_blocks(int narrow, int wide, float wide_cost, int blocks) {
     if (narrow == 0) return 0;
     if (wide == 0) return blocks;
-    const float a = 4.f * static_cast<float>(narrow), b = kTreeWideCost * static_cast<float>(wide);
-    const int n = static_cast<int>(blocks * (a / (a + b)) + 0.5f);
+    const float a = 4.f * static_cast<float>(narrow);
+    const int n = static_cast<int>(blocks * (a / (a + wide_cost)) + 0.5f);
     return tree_max(1, tree_min(n, blocks - 1));
 }
 
