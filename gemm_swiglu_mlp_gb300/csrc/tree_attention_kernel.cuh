@@ -69,7 +69,8 @@ struct TreeAttnArgs {
     uint16_t *out;                     // [tokens][q heads][D]
     float4 *partial;                   // [2 * grid][D / 4][part_rows], four columns a row
     float2 *stats;                     // [2 * grid][part_rows]: maximum, sum
-    int4 *chains;                      // [grid]: items that begin in a block and go on
+    int4 *chains;                      // [grid]: an item that goes on in the next block: its blocks
+                                       // first | last << 16, first token, kv head, tokens (0: none)
     long long max_pages;
     float scale_log2;                  // scale * log2(e)
     int q_heads, num_pages, page_shift, mask_words;
@@ -682,14 +683,17 @@ __device__ __forceinline__ void tree_describe(const TreeAttnArgs &a, const TreeB
         w.entry(g, load, e);
         flags[2 * i] = flags[2 * i + 1] = 0;
         more = e->steps > 0;
-        // an item that begins here and goes on in the next blocks
-        for (int s = 0; s < 2 && more; ++s) {
+        // an item that goes on in the next block (of a Split or Pair in part 0)
+        for (int s = 0; s < (e->kind == kTreeDuo ? 2 : 1) && more; ++s) {
             const TreePart &x = e->part[s];
-            if ((x.flags & (kPartWhole | kPartBegins | kPartSecond)) != kPartBegins) continue;
             const int rest = (x.len + kTreeTile - 1) / kTreeTile - x.end;
+            if (rest == 0) continue;
             const int last = tree_block_begin(blk.cut, blk.index + 1) + rest - 1;
-            chain = make_int4(blk.base + tree_block_of(blk.cut, last), x.tok, x.h,
-                              x.ntok + (e->kind == kTreePair ? e->part[1].ntok : 0));
+            const int first = (x.flags & kPartBegins)
+                                  ? blk.index
+                                  : tree_block_of(blk.cut, tree_block_begin(blk.cut, blk.index) - x.first);
+            chain = make_int4((blk.base + first) | (blk.base + tree_block_of(blk.cut, last)) << 16, x.tok,
+                              x.h, x.ntok + (e->kind == kTreePair ? e->part[1].ntok : 0));
         }
         mbar_arrive(bars.e_full(i));
     }
@@ -1467,41 +1471,53 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // ---------------------------------------------------------------- partial results
-constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 8;   // blocks a chain
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinBlocks = 8;   // for each block whose item goes on in the next
 
 // Items that several blocks worked on: out = sum_b w_b o_b / sum_b w_b l_b,
-// w_b = exp(scale * (m_b - max m)), in block order, so that the result does
-// not depend on which block finished first. Blocks (c, 0..) sum the item that
-// begins in block c, if one does; a warp takes 32 rows (a lane each: partial
-// results lie with the rows next to each other) and eight columns.
+// w_b = exp(scale * (m_b - max m)), in an order that depends on the item alone,
+// not on which block finished first. A task is 32 rows (a lane each: partial
+// results lie with the rows next to each other) and eight columns. An item of p
+// blocks has kJoinBlocks * (p - 1) blocks here, and as these grow more than its
+// tasks, up to eight warps share a task's partial results. Measured, one request
+// of 2 kv heads with 7 heads each, context 16000 (76 blocks an item), the call: one
+// token 46 us with kJoinBlocks blocks an item and one warp a task, 20 so; 18
+// tokens 77 and 23.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a) {
+    __shared__ float shares[kJoinWarps][10][32];   // maximum, sum, eight columns
     griddep_launch_dependents();
     griddep_wait();
-    const int c = static_cast<int>(blockIdx.x), lane = threadIdx.x & 31;
-    const int4 chain = a.chains[c];   // last block, first token, head, tokens (0: none)
+    const int4 chain = a.chains[blockIdx.x];
     if (chain.w == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = chain.x & 0xFFFF, parts = (chain.x >> 16) - c + 1;
     const int tpt = a.geom.tpt, group = a.geom.group;
-    const int parts = chain.x - c + 1;
     const int rows = chain.w * group;
-    const int groups = (rows + 31) / 32;
-    for (int task = static_cast<int>(blockIdx.y) * (kJoinThreads / 32) + (threadIdx.x >> 5);
-         task < groups * (D / 8); task += kJoinBlocks * (kJoinThreads / 32)) {
+    const int groups = (rows + 31) / 32, tasks = groups * (D / 8);
+    const int helpers = kJoinBlocks * (parts - 1);
+    const int helper = kJoinBlocks * (static_cast<int>(blockIdx.x) - c) + static_cast<int>(blockIdx.y);
+    // warps a task: as there is room, each with two partial results at least
+    int sharers = 1;
+    while (2 * sharers <= kJoinWarps && 4 * sharers <= parts && 2 * sharers * tasks <= kJoinWarps * helpers)
+        sharers *= 2;
+    const int at_once = kJoinWarps / sharers, part = warp % sharers;
+    for (int base = helper * at_once; base < tasks; base += helpers * at_once) {
+        const int task = base + warp / sharers;
         const int col = task / groups * 8, i = (task % groups) * 32 + lane;
-        if (i >= rows) continue;
         const int tok = i / group, head = i - tok * group;
         const int second = tok >= tpt;
         const int row = 128 * second + (tok - second * tpt) * group + head;
+        const bool on = task < tasks && i < rows;
         // part 0 is the slot of an item that begins in c, the others' of one that goes on
         float top = -INFINITY;
-        for (int b = 0; b < parts; ++b) {
+        for (int b = part; on && b < parts; b += sharers) {
             const long long slot = b == 0 ? 2 * c + 1 : 2 * (c + b);
             top = fmaxf(top, a.stats[slot * a.part_rows + row].x);
         }
         float acc[8] = {}, l = 0.f;
-#pragma unroll 2
-        for (int b = 0; b < parts; ++b) {
+#pragma unroll 1
+        for (int b = part; on && b < parts; b += sharers) {
             const long long slot = b == 0 ? 2 * c + 1 : 2 * (c + b);
             const float2 st = a.stats[slot * a.part_rows + row];
             const float4 *o = a.partial + (slot * (D / 4) + col / 4) * a.part_rows + row;
@@ -1517,6 +1533,34 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
             acc[6] = fmaf(y.z, f, acc[6]);
             acc[7] = fmaf(y.w, f, acc[7]);
         }
+        if (sharers > 1) {   // the first of them adds the others' shares
+            float(*mine)[32] = shares[warp];
+            if (part) {
+                mine[0][lane] = top;
+                mine[1][lane] = l;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mine[2 + e][lane] = acc[e];
+            }
+            __syncthreads();
+            if (part == 0) {
+                float now = top;
+                for (int w = 1; w < sharers; ++w) now = fmaxf(now, mine[10 * w][lane]);
+                const float f = top == -INFINITY ? 0.f : ex2((top - now) * a.scale_log2);
+                l *= f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll 1
+                for (int w = 1; w < sharers; ++w) {
+                    const float m = mine[10 * w][lane];
+                    const float fw = m == -INFINITY ? 0.f : ex2((m - now) * a.scale_log2);
+                    l = fmaf(mine[10 * w + 1][lane], fw, l);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(mine[10 * w + 2 + e][lane], fw, acc[e]);
+                }
+            }
+            __syncthreads();
+        }
+        if (!on || part) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint32_t p[4];
 #pragma unroll
