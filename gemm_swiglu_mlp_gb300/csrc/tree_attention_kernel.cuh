@@ -41,10 +41,23 @@
 // In both the accumulator is only rescaled when the maximum has risen by more
 // than 2^8, so most tiles leave it alone and weights stay below 2^8.
 // TMEM: scores of the two groups in columns 0-255, the two accumulators in
-// 256 + D each (narrow: sums of p v in 32 columns, sums of p in 32). While one group's softmax runs, the tensor cores work for the
-// other; how an entry gives both groups work is said at TreeEntry.
+// 256 + D each (narrow: sums of p v in 32 columns, sums of p in 32). While one
+// group's softmax runs, the tensor cores work for the other; how an entry gives
+// both groups work is said at TreeEntry.
 // Every wait is bounded (sm103_ptx.cuh); a group's barriers are reached by all
 // of its warps whatever their waits said.
+//
+// What bounds it. Narrow, with enough requests: the bytes of K and V (64
+// requests of one token, contexts of 4000, 4 kv heads of 128: 5.6 TB/s of
+// K and V over the whole call, pages of 64 rows). Wide, two row tiles an item:
+// the chain of one tile - scores 512 clocks of the tensor cores, softmax 1900,
+// result 512, and some 1000 of waits, barriers and issue between them - which
+// two groups can only half overlap, as TMEM holds no third tile's scores (32
+// requests of up to 64 tokens, 8 heads a kv head, contexts of 2000 to 6000:
+// 268 us, 742 TFLOP/s of products that count). No single piece of it is the
+// bound: without the exponentials, or half of either product, it takes 4%
+// less. Small calls: 6 us are launch, the shares' prologue and the end of the
+// kernel, 2 to 3 the join.
 //
 // Five roles run different code at once, and the SM's instruction cache holds
 // some 32 KB: the roles read what they follow from shared memory instead of

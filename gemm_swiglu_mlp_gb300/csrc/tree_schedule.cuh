@@ -7,10 +7,10 @@
 // up to two such row tiles (2 * tpt tokens) of one (request, kv head), against
 // the positions its tokens can see, in TILES of 128 positions. Items are
 // numbered request by request, then kv head, then token block, and all tiles
-// of all items form one line of `total` units; block c of `blocks` takes the
-// units [total * c / blocks, total * (c + 1) / blocks), whatever items they
-// belong to. So ragged lengths balance to one tile, and an item that crosses
-// a block boundary is summed from the blocks' partial results.
+// of all items of one form (tree_is_narrow) are one line of `total` units; each
+// of the form's blocks takes as many of them, to one unit, whatever items they
+// belong to (tree_cut). So ragged lengths balance to one tile, and an item that
+// crosses a block boundary is summed from the blocks' partial results.
 #pragma once
 
 #include <cstdint>

@@ -285,6 +285,19 @@ def test_attention_long_contexts(sg, ctx, new, Hq, Hkv, D, P, tree):
     c.check(c.run(sg))
 
 
+@pytest.mark.parametrize("D,P", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_items_of_two_to_many_blocks(sg, D, P, tree):
+    """One long line of work: items of one, two, some and many blocks, of a few
+    rows, one row tile and two, in both forms."""
+    ctx = [300, 6000, 900, 50, 1500, 2500, 100, 4000, 0, 3000]
+    new = [1, 3, 20, 40, 2, 33, 9, 1, 5, 64]
+    c = Case(D + tree, ctx, new, 8, 1, D, P, tree)
+    c.check(c.run(sg))
+    c = Case(D + tree + 2, ctx[::-1], new, 7, 1, D, P, tree)
+    c.check(c.run(sg))
+
+
 def test_attention_many_requests(sg):
     rng = np.random.default_rng(5)
     new = rng.integers(0, 4, 300)
