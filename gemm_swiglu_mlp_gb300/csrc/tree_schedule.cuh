@@ -68,6 +68,10 @@ SWIGLU_HD TreeReq tree_request(const TreeGeom &g, int start, int end, int ctx) {
 // Requests of up to this many rows a kv head are worked on in the kernel's
 // narrow form, the others in its wide form, by blocks of their own: each form
 // has a line of work with only its requests on it.
+// Measured (us, narrow / wide, 2 kv heads of 7 heads of 128): 300 requests of one
+// token 17 / 20 at contexts of 100 and 116 / 125 at 2000, of four tokens (28 rows)
+// 23 / 20, 48 / 47 at 500 and 125 / 129; 10 requests of four tokens 12.0 / 12.5 and
+// 18.4 / 18.6.
 constexpr int kTreeNarrow = 32;
 SWIGLU_HD bool tree_is_narrow(const TreeGeom &g, const TreeReq &q) {
     return q.n <= kTreeNarrow && q.n * g.group <= kTreeNarrow;
