@@ -622,39 +622,47 @@ __device__ __forceinline__ void tree_mend_v(const TreeBlock &blk) {
             const TreePart &x = e->part[s];
             const int tile = x.tile(step);
             if (!is_k && x.edge(tile)) {
-                // rows [first, end) hold new tokens, [end, 128) nothing (of
-                // which the product reads those up to a multiple of 16); a
-                // row's 16-byte chunks are permuted within its 128 bytes
+                // Rows [first, end) hold new tokens, [end, 128) nothing (of
+                // which the product reads those up to a multiple of 16). In
+                // the order of memory, 256 chunks of 16 bytes at a time, eight
+                // loads in flight a lane: with one a tile of new tokens took
+                // 6400 clocks, longer than its softmax.
                 const int end = tree_min(x.len - tile * kTreeTile, kTreeTile);
                 const int first = tree_min(tree_max(x.ctx - tile * kTreeTile, 0), end);
                 const int stop = (end + 15) & ~15;
-                uint8_t *base = blk.smem + C::OFF_KV + k.stage * C::TILE;
-                constexpr int chunks = C::HALVES * 8;   // a row
+                uint4 *base = reinterpret_cast<uint4 *>(blk.smem + C::OFF_KV + k.stage * C::TILE);
+                constexpr int per_group = C::GROUP / 16;   // chunks of eight rows
+                auto row_of = [](int m) { return m / per_group * 8 + (m >> 3 & 7); };
                 bool bad = false;
 #pragma unroll 1
-                for (int i = first * chunks + lane; i < stop * chunks; i += 32) {
-                    const int r = i / chunks, c = i % chunks;
-                    uint4 *at = reinterpret_cast<uint4 *>(base + (r >> 3) * C::GROUP +
-                                                          (c >> 3) * 1024 + (r & 7) * kRowBytes +
-                                                          (c & 7) * 16);
-                    if (r >= end) {
-                        *at = make_uint4(0, 0, 0, 0);
-                        continue;
+                for (int m0 = ((first >> 3) * per_group & ~255) + lane; row_of(m0) < end; m0 += 256) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) v[u] = base[m0 + 32 * u];
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int r = row_of(m0 + 32 * u);
+                        // exponent all ones: carry
+                        const uint32_t x = ((v[u].x & 0x7F807F80u) + 0x00800080u) |
+                                           ((v[u].y & 0x7F807F80u) + 0x00800080u) |
+                                           ((v[u].z & 0x7F807F80u) + 0x00800080u) |
+                                           ((v[u].w & 0x7F807F80u) + 0x00800080u);
+                        any |= r >= first && r < end ? x : 0u;
                     }
-                    const uint4 v = *at;
-                    // exponent all ones: carry
-                    const uint32_t any = ((v.x & 0x7F807F80u) + 0x00800080u) |
-                                         ((v.y & 0x7F807F80u) + 0x00800080u) |
-                                         ((v.z & 0x7F807F80u) + 0x00800080u) |
-                                         ((v.w & 0x7F807F80u) + 0x00800080u);
                     if (any & 0x80008000u) {
                         bad = true;
-                        uint16_t *h = reinterpret_cast<uint16_t *>(at);
 #pragma unroll 1
-                        for (int j = 0; j < 8; ++j)
-                            if ((h[j] & 0x7F80u) == 0x7F80u) h[j] = 0;
+                        for (int u = 0; u < 64; ++u) {   // value u % 8 of chunk u / 8
+                            const int m = m0 + 32 * (u >> 3), r = row_of(m);
+                            uint16_t *h = reinterpret_cast<uint16_t *>(base + m) + (u & 7);
+                            if (r >= first && r < end && (*h & 0x7F80u) == 0x7F80u) *h = 0;
+                        }
                     }
                 }
+#pragma unroll 1
+                for (int m = (end >> 3) * per_group + lane; row_of(m) < stop; m += 32)
+                    if (row_of(m) >= end) base[m] = make_uint4(0, 0, 0, 0);
                 if (bad) {
                     volatile int *flags = tree_flags<D>(blk.smem) + 2 * (e - k.entries);
                     flags[s] = 1;
