@@ -511,14 +511,14 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
     };
     bool ok = fetch();
     while (ok) {
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < 2; ++s) {
             if (!ok) break;
             bool k_there = false;
-            if (step < cur.tiles[s]) {   // the result's product
+            if (step < (s ? cur.tiles[1] : cur.tiles[0])) {   // the result's product
                 if (s == 0 || cur.kind != kTreePair) {
                     ok = next_stage(vstage);
-                    if (ok && step >= cur.edge[s]) {
+                    if (ok && step >= (s ? cur.edge[1] : cur.edge[0])) {
                         ok = tree_wait(bars.v_fixed(vstage), (fphase >> vstage) & 1u, abort_flag);
                         fphase ^= 1u << vstage;
                     }
@@ -534,9 +534,9 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                 const uint32_t acc = blk.tmem + TreeShared<D>::TMEM_O + D * s;
                 constexpr uint32_t kstep = 2 * C::GROUP >> 4;   // 16 positions of V
                 const uint32_t more = step != 0;
-                const bool last = step + 1 == cur.tiles[s];
+                const bool last = step + 1 == (s ? cur.tiles[1] : cur.tiles[0]);
                 // positions of the tile, in 16s (the rest has no weight)
-                const int count = last ? cur.tail[s] : kTreeTile / 16;
+                const int count = last ? (s ? cur.tail[1] : cur.tail[0]) : kTreeTile / 16;
 #pragma unroll
                 for (int i = 0; i < kTreeTile / 16; ++i) {
                     if (i >= count) break;
@@ -554,7 +554,7 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                 if (s == 1 || cur.kind != kTreePair) umma_commit(bars.kv_empty(vstage));
                 if (last) umma_commit(bars.o_full(s));
             }
-            if (nstep < nxt.tiles[s]) {   // the next scores
+            if (nstep < (s ? nxt.tiles[1] : nxt.tiles[0])) {   // the next scores
                 const bool two_q = nxt.kind != kTreeSplit;
                 const int buf = two_q ? qb ^ s : qb;
                 if (nstep == 0 && (s == 0 || two_q)) {
@@ -578,7 +578,7 @@ __device__ __forceinline__ void tree_issue(const TreeBlock &blk) {
                 if (s == 1 || nxt.kind != kTreePair) umma_commit(bars.kv_empty(kstage));
                 // the last scores that need this Q tile: the part's, in a split
                 // those of the entry's last tile
-                const bool last = nstep + 1 == nxt.tiles[s];
+                const bool last = nstep + 1 == (s ? nxt.tiles[1] : nxt.tiles[0]);
                 if (two_q ? last : nstep + 1 == nxt.steps && (s == 1 || nstep >= nxt.tiles[1]))
                     umma_commit(bars.q_empty(buf));
             }
