@@ -456,6 +456,9 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     a.page_shift = shape.page_shift;
     a.mask_words = static_cast<int>(mask_words);
     a.part_rows = ws.rows;
+#ifdef SWIGLU_TEST_FAULT_INJECTION
+    a.skip_first_fill = g_test_skip_first_fill;
+#endif
     const uint64_t pages_heads = static_cast<uint64_t>(num_pages) * static_cast<uint64_t>(kv_heads);
     CUtensorMap tmQ, tmQn, tmK, tmV;
     const uint64_t D = static_cast<uint64_t>(head_dim);

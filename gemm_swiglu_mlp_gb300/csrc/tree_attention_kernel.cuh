@@ -64,7 +64,7 @@
 // keeping copies, have one call site for each kind of step, and leave loops
 // rolled where a step is long anyway (with everything inlined and unrolled,
 // 290 KB, a quarter of the fetches missed and warps waited longer for
-// instructions than for scores).
+// instructions than for scores; now 153 KB and a tenth).
 #pragma once
 
 #include "epilogue.cuh"
@@ -88,6 +88,9 @@ struct TreeAttnArgs {
     float scale_log2;                  // scale * log2(e)
     int q_heads, num_pages, page_shift, mask_words;
     int part_rows;                     // rows of one partial result: 128 or 256
+#ifdef SWIGLU_TEST_FAULT_INJECTION
+    int skip_first_fill;               // test build only: never fill the first pipeline stage
+#endif
 };
 
 constexpr int kTreeEntries = 4;   // entries described ahead of their results
@@ -438,6 +441,14 @@ __device__ __forceinline__ uint2 tree_produce(const CUtensorMap &tmQ, const CUte
             }
             ok = warp_wait(bars.kv_empty(k.stage), k.phase ^ 1u, abort_flag);
             if (!ok) break;
+#ifdef SWIGLU_TEST_FAULT_INJECTION
+            // test build: leave the first stage unfilled, so that the waits for
+            // it run out
+            if (a.skip_first_fill && k.stage == 0 && k.phase == 0) {
+                k.advance();
+                continue;
+            }
+#endif
             if (lane == 0)
                 mbar_arrive_expect_tx(bars.kv_full(k.stage), static_cast<uint32_t>(count) *
                                                                  kRowBytes * C::HALVES
@@ -988,9 +999,9 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
         if (lane == 0) mbar_arrive(bars.o_done());
         ph.merged = true;
         ph.merge ^= 1u;
-    } else {
-        group_sync(s);   // the maxima have been read
     }
+    // (no barrier of the group after a way out: tree_softmax has the one that
+    // comes before the statistics are used again)
     return true;
 }
 
@@ -1241,9 +1252,9 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
         if (lane == 0) mbar_arrive(bars.o_done());
         ph.merged = true;
         ph.merge ^= 1u;
-    } else {
-        group_sync(s);   // the sums have been read
     }
+    // (no barrier of the group after a way out: tree_softmax has the one that
+    // comes before the statistics are used again)
     return true;
 }
 
