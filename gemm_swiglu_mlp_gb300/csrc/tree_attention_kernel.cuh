@@ -1511,10 +1511,11 @@ constexpr int kJoinBlocks = 8;   // for each block whose item goes on in the nex
 // not on which block finished first. A task is 32 rows (a lane each: partial
 // results lie with the rows next to each other) and eight columns. An item of p
 // blocks has kJoinBlocks * (p - 1) blocks here, and as these grow more than its
-// tasks, up to eight warps share a task's partial results. Measured, one request
-// of 2 kv heads with 7 heads each, context 16000 (76 blocks an item), the call: one
-// token 46 us with kJoinBlocks blocks an item and one warp a task, 20 so; 18
-// tokens 77 and 23.
+// tasks, up to eight warps share a task's partial results, and with few rows the
+// lanes that these leave over. Measured, one request of 2 kv heads with 7 heads
+// each, context 16000 (76 blocks an item), the call: one token 46 us with
+// kJoinBlocks blocks an item and one warp a task, 20 with the warps, 17 with the
+// lanes too; 18 tokens 77 and 23.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnArgs a) {
     __shared__ float shares[kJoinWarps][10][32];   // maximum, sum, eight columns
@@ -1534,22 +1535,29 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
     while (2 * sharers <= kJoinWarps && 4 * sharers <= parts && 2 * sharers * tasks <= kJoinWarps * helpers)
         sharers *= 2;
     const int at_once = kJoinWarps / sharers, part = warp % sharers;
+    // and the lanes that the rows leave over, as long as two are left for each:
+    // adding up a share costs about as much as reading a partial result
+    int slots = 32;
+    if (sharers > 1)
+        while (slots >= 2 * rows && sharers * (32 / slots) * 4 <= parts) slots >>= 1;
+    const int lane_row = lane & (slots - 1), stride = sharers * (32 / slots);
+    const int first = part * (32 / slots) + lane / slots;
     for (int base = helper * at_once; base < tasks; base += helpers * at_once) {
         const int task = base + warp / sharers;
-        const int col = task / groups * 8, i = (task % groups) * 32 + lane;
+        const int col = task / groups * 8, i = (task % groups) * 32 + lane_row;
         const int tok = i / group, head = i - tok * group;
         const int second = tok >= tpt;
         const int row = 128 * second + (tok - second * tpt) * group + head;
         const bool on = task < tasks && i < rows;
         // part 0 is the slot of an item that begins in c, the others' of one that goes on
         float top = -INFINITY;
-        for (int b = part; on && b < parts; b += sharers) {
+        for (int b = first; on && b < parts; b += stride) {
             const long long slot = b == 0 ? 2 * c + 1 : 2 * (c + b);
             top = fmaxf(top, a.stats[slot * a.part_rows + row].x);
         }
         float acc[8] = {}, l = 0.f;
 #pragma unroll 1
-        for (int b = part; on && b < parts; b += sharers) {
+        for (int b = first; on && b < parts; b += stride) {
             const long long slot = b == 0 ? 2 * c + 1 : 2 * (c + b);
             const float2 st = a.stats[slot * a.part_rows + row];
             const float4 *o = a.partial + (slot * (D / 4) + col / 4) * a.part_rows + row;
@@ -1567,32 +1575,31 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeAttnA
         }
         if (sharers > 1) {   // the first of them adds the others' shares
             float(*mine)[32] = shares[warp];
-            if (part) {
-                mine[0][lane] = top;
-                mine[1][lane] = l;
+            mine[0][lane] = top;
+            mine[1][lane] = l;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mine[2 + e][lane] = acc[e];
-            }
+            for (int e = 0; e < 8; ++e) mine[2 + e][lane] = acc[e];
             __syncthreads();
-            if (part == 0) {
+            if (part == 0 && lane < slots) {
                 float now = top;
-                for (int w = 1; w < sharers; ++w) now = fmaxf(now, mine[10 * w][lane]);
-                const float f = top == -INFINITY ? 0.f : ex2((top - now) * a.scale_log2);
-                l *= f;
+                for (int w = 0; w < stride; ++w)
+                    now = fmaxf(now, mine[10 * (w & (sharers - 1))][lane + w / sharers * slots]);
+                l = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] *= f;
+                for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll 1
-                for (int w = 1; w < sharers; ++w) {
-                    const float m = mine[10 * w][lane];
+                for (int w = 0; w < stride; ++w) {
+                    const int other = 10 * (w & (sharers - 1)), at = lane + w / sharers * slots;
+                    const float m = mine[other][at];
                     const float fw = m == -INFINITY ? 0.f : ex2((m - now) * a.scale_log2);
-                    l = fmaf(mine[10 * w + 1][lane], fw, l);
+                    l = fmaf(mine[other + 1][at], fw, l);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(mine[10 * w + 2 + e][lane], fw, acc[e]);
+                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(mine[other + 2 + e][at], fw, acc[e]);
                 }
             }
             __syncthreads();
         }
-        if (!on || part) continue;
+        if (!on || part || lane >= slots) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint32_t p[4];
 #pragma unroll
