@@ -216,7 +216,7 @@ __device__ __forceinline__ uint32_t mask_of_bits(int n) {   // the n lowest bits
     return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
 }
 
-// What a token's row of the mask is judged by.
+// What decides which positions a token sees.
 struct TreeSight {
     const unsigned long long *mask;   // the token's words, or null: causal
     int words;
