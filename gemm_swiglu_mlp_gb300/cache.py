@@ -27,13 +27,10 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import SWIGLU_ERR_INVALID_ARG, SwigluError, load_library
+from . import SwigluError, load_library
 from .build import BINDING_PATH
 
 _binding = None
-# (device index, stream handle) -> uint8 tensor; apart from the other entry
-# points' workspaces, whose counters have to stay as they are between calls
-_workspaces = {}
 
 
 def _native():
@@ -58,19 +55,10 @@ def _native():
 
 
 def _workspace(index: int, nbytes: int, stream) -> torch.Tensor:
-    """A new attention workspace for a (device, stream) that has none, or a
-    smaller one."""
-    if torch.cuda.is_current_stream_capturing():
-        # an allocation made during capture belongs to the graph's pool
-        raise SwigluError(SWIGLU_ERR_INVALID_ARG,
-                          "this call needs a workspace of %d bytes: allocate it before "
-                          "capturing (swiglu_tree_attention_workspace_bytes) and pass "
-                          "workspace=" % nbytes)
+    """A new attention workspace, allocated as `stream`'s own (None: the current
+    one's); while that stream is being captured, out of the graph's pool."""
     with torch.cuda.device(index), torch.cuda.stream(stream):
-        ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-        key = (index, torch.cuda.current_stream().cuda_stream)
-    _workspaces[key] = ws
-    return ws
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
 def _on(stream, f, *args):

@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -133,6 +134,15 @@ void *stream_of(PyObject *stream, int index) {
     return p;
 }
 
+bool capturing(void *stream) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &status) != cudaSuccess) {
+        cudaGetLastError();   // (of a stream that no call may use now: its launch reports it)
+        return true;
+    }
+    return status != cudaStreamCaptureStatusNone;
+}
+
 int64_t integer(PyObject *o) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Refused{};
@@ -230,7 +240,10 @@ PyObject *write(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // One attention workspace per (device, stream), made by cache.py and grown on
-// demand; kept to the process's end.
+// demand; kept to the process's end. No captured call uses it: a graph holds the
+// address, which growing would leave to the allocator, and may be replayed on
+// another stream beside this one's calls. Apart from the other entry points'
+// workspaces, whose counters have to stay as they are between calls.
 using Workspaces = std::map<std::pair<int, void *>, Tensor>;
 Workspaces &workspaces() {
     static Workspaces *all = new Workspaces;   // (not destroyed after CUDA at exit)
@@ -277,6 +290,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const size_t need = g_attend_bytes(T, heads, c.heads, c.dim);
     void *ws = nullptr;
     size_t ws_bytes = 0;
+    Tensor captured;   // a captured call's: the graph's pool has it back after this call's launches
     if (a[9] != Py_None) {
         if (!THPVariable_Check(a[9]) || !THPVariable_Unpack(a[9]).is_cuda())
             refuse(PyExc_TypeError, "%s must be a CUDA tensor", "workspace");
@@ -284,7 +298,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         ws = w.data_ptr();
         ws_bytes = w.nbytes();
     } else if (need) {
-        Tensor &w = workspaces()[{c.index, stream}];
+        Tensor &w = capturing(stream) ? captured : workspaces()[{c.index, stream}];
         if (!w.defined() || w.nbytes() < need) {
             PyObject *o = PyObject_CallFunction(g_workspace, "inO", c.index,
                                                 static_cast<Py_ssize_t>(need), a[10]);
