@@ -76,6 +76,7 @@ EXPORTED_SYMBOLS = (
 _lock = threading.Lock()
 _lib = None
 _workspaces = {}   # (device index, stream handle) -> zero-initialised uint8 tensor
+_outgrown = []     # earlier ones, which captured graphs may still use
 _ws_bytes = {}     # ([entry,] device index, M, N, K, kernel and schedule overrides) -> bytes
 
 
@@ -309,18 +310,26 @@ def _default_workspace(device, nbytes: int, stream) -> torch.Tensor:
     """One zero-filled workspace per (device, stream), grown on demand. Calls
     on one stream run one after another, and each completed call leaves the
     workspace's counters at zero, so reuse across calls and shapes is safe.
-    The zero fill is ordered on the same stream as the calls that use it."""
+    The zero fill is ordered on the same stream as the calls that use it.
+
+    A graph captured with it holds its address, so one that has been outgrown
+    is kept; each is at least twice the one before, so those come to less than
+    the one in use. Replays use the capture stream's workspace: those that may
+    run beside that stream's other calls need a workspace of their own."""
     dev = torch.device(device)
     s = torch.cuda.current_stream(dev) if stream is None else stream
     key = (dev.index, int(s.cuda_stream))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        if torch.cuda.is_current_stream_capturing():
-            # an allocation made during capture belongs to the graph's pool
-            raise SwigluError(SWIGLU_ERR_INVALID_ARG,
-                              "this shape needs a workspace of %d bytes: allocate it before "
-                              "capturing (swiglu_workspace_bytes) and pass workspace=" % nbytes)
         with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                # an allocation made during capture belongs to the graph's pool
+                raise SwigluError(SWIGLU_ERR_INVALID_ARG,
+                                  "this shape needs a workspace of %d bytes: allocate it before "
+                                  "capturing (swiglu_workspace_bytes) and pass workspace=" % nbytes)
+            if ws is not None:
+                _outgrown.append(ws)
+                nbytes = max(nbytes, 2 * ws.numel())
             ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
         _workspaces[key] = ws
     return ws
