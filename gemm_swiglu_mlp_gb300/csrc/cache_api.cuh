@@ -450,7 +450,9 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     a.stats = reinterpret_cast<float2 *>(base + ws.stats);
     a.partial = reinterpret_cast<float4 *>(base + ws.partial);
     a.max_pages = max_pages;
-    a.scale_log2 = scale * 1.4426950408889634f;   // log2(e)
+    // (finite, also from the largest and the smallest scales)
+    a.scale_log2 = std::min(scale * 1.4426950408889634f, FLT_MAX);   // log2(e)
+    a.rise = std::min(kTreeRescale / a.scale_log2, FLT_MAX);
     a.q_heads = static_cast<int>(q_heads);
     a.num_pages = static_cast<int>(num_pages);
     a.page_shift = shape.page_shift;

@@ -86,6 +86,7 @@ struct TreeAttnArgs {
                                        // first | last << 16, first token, kv head, tokens (0: none)
     long long max_pages;
     float scale_log2;                  // scale * log2(e)
+    float rise;                        // kTreeRescale / scale_log2: a rise of the maximum, as a score
     int q_heads, num_pages, page_shift, mask_words;
     int part_rows;                     // rows of one partial result: 128 or 256
 #ifdef SWIGLU_TEST_FAULT_INJECTION
@@ -186,6 +187,22 @@ __device__ __forceinline__ volatile int *tree_flags(uint8_t *smem) {
 }
 
 constexpr float kTreeRescale = 8.f;   // rise of the maximum (log2) that rescales
+
+// Scores of any finite size. "Has outgrown the maximum" compares scores, score >
+// maximum + rise, which holds for every finite score while there is no maximum
+// (-inf), and a weight of the maximum itself must not be a rounding error's:
+// (score - maximum) * scale is exactly 0 for it. The wide form spends one
+// multiply-add a score, score * scale - maximum * scale, whose second product is
+// rounded: by up to 64 at 2^31, and past that the rounding alone could take
+// weights out of range. There neighbouring scores are 2^7 or more apart, so all
+// but the maximum have no weight, which any large factor gives: one that is a power
+// of two and takes the maximum to 2^30 rounds nothing.
+__device__ __forceinline__ float tree_factor(float max, float scale) {
+    constexpr float kLarge = 2147483648.f;
+    const uint32_t exponent = (__float_as_uint(max) >> 23) & 255u;
+    return max != -INFINITY && fabsf(max * scale) >= kLarge ? __uint_as_float((284u - exponent) << 23)
+                                                            : scale;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -778,11 +795,10 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
     volatile int *abort_flag = tree_abort<D>(blk.smem);
     volatile int *flags = tree_flags<D>(blk.smem);
     // a group's statistics: its warps' maxima [4][32], the maximum [32], its
-    // last rescale factor [32], and what is added to scale * score [32]:
-    // -scale * maximum, or a number that makes any score rise while there is
-    // no maximum
-    constexpr int kMax = 128, kFactor = 160, kAdd = 192;
-    constexpr float kNoMax = 1e30f;
+    // last rescale factor [32], what is taken off a score (the maximum, or 0
+    // while there is none) [32], and the score above which a row has outgrown
+    // its maximum [32]
+    constexpr int kMax = 128, kFactor = 160, kBase = 192, kTop = 224;
     float *group_stats = tree_stats<D>(blk.smem) + 256 * s;
     const TreePart &x = entry.part[s];
     const int rows = x.ntok * g.group;
@@ -797,7 +813,8 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
     if (!tree_results_read<D>(bars, ph, abort_flag)) give_up();
     if (warp == 8 * s) {
         group_stats[kMax + lane] = -INFINITY;
-        group_stats[kAdd + lane] = kNoMax;
+        group_stats[kBase + lane] = 0.f;
+        group_stats[kTop + lane] = -INFINITY;
     }
     uint8_t *const weights = blk.smem + C::OFF_W + s * C::W_BYTES + row * (2 * kTreeNarrow);
     const int swizzle = 16 * ((row >> 1) & 3);   // 64-byte rows, 64-byte swizzle
@@ -841,16 +858,20 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
             for (int n0 = 8 * half; n0 < rows && good; n0 += 16) {
                 uint32_t v[8];
                 scores(n0, v);
-                float add[8];
-                *reinterpret_cast<float4 *>(add) =
-                    *reinterpret_cast<const float4 *>(group_stats + kAdd + n0);
-                *reinterpret_cast<float4 *>(add + 4) =
-                    *reinterpret_cast<const float4 *>(group_stats + kAdd + n0 + 4);
+                float base[8], above[8];
+#pragma unroll
+                for (int n = 0; n < 8; n += 4) {
+                    *reinterpret_cast<float4 *>(base + n) =
+                        *reinterpret_cast<const float4 *>(group_stats + kBase + n0 + n);
+                    *reinterpret_cast<float4 *>(above + n) =
+                        *reinterpret_cast<const float4 *>(group_stats + kTop + n0 + n);
+                }
                 float e[8];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                    e[n] = fmaf(__uint_as_float(v[n]), sc, first ? kNoMax : add[n]);
-                    rise = rise || (n0 + n < rows && e[n] > kTreeRescale);
+                    const float score = __uint_as_float(v[n]);
+                    e[n] = (score - (first ? 0.f : base[n])) * sc;
+                    rise = rise || (n0 + n < rows && score > (first ? -INFINITY : above[n]));
                 }
                 uint32_t p[4];
 #pragma unroll
@@ -858,7 +879,7 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
                 *reinterpret_cast<uint4 *>(weights + ((2 * n0) ^ swizzle)) =
                     make_uint4(p[0], p[1], p[2], p[3]);
             }
-            // (once a tile: scores of 1e9 and more can be past it by rounding)
+            // (once a tile: nothing is above the new maximum)
             const bool risen = group_any(s, rise && good && again);
             if (*abort_flag) good = false;
             if (!risen) break;
@@ -884,7 +905,8 @@ __device__ __forceinline__ bool tree_narrow_part(const TreeAttnArgs &a, const Tr
                                         old);
                 group_stats[kMax + lane] = top;
                 group_stats[kFactor + lane] = top > old ? ex2((old - top) * sc) : 1.f;
-                group_stats[kAdd + lane] = top == -INFINITY ? kNoMax : -top * sc;
+                group_stats[kBase + lane] = top == -INFINITY ? 0.f : top;
+                group_stats[kTop + lane] = top + a.rise;
             }
             group_sync(s);
             if (!first && tile != x.first) {
@@ -1082,7 +1104,7 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
                 top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             }
         }
-        const bool rise = fresh || (row_on && top * sc > m * sc + kTreeRescale);
+        const bool rise = fresh || (row_on && top > m + a.rise);
         const bool risen = group_any(s, rise && good);
         if (*abort_flag) good = false;
         if (risen) {
@@ -1091,7 +1113,7 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
             const float2 both = stats[row];
             const float now = fmaxf(both.x, both.y);
             float f = 1.f;
-            if (now > m && (fresh || now * sc > m * sc + kTreeRescale)) {
+            if (now > m && (fresh || now > m + a.rise)) {
                 f = ex2((m - now) * sc);
                 m = now;
                 l *= f;
@@ -1112,7 +1134,8 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
         }
         if (warp_on) {
             // no maximum so far: weights 2^(-inf - 0) = 0
-            const float base = m == -INFINITY ? 0.f : -m * sc;
+            const float by = tree_factor(m, sc);
+            const float base = m == -INFINITY ? 0.f : -m * by;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
             for (int i = 1; i >= 0; --i) {
@@ -1121,7 +1144,7 @@ __device__ __forceinline__ bool tree_wide_part(const TreeAttnArgs &a, const Tree
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     float lo, hi;
-                    fma2(lo, hi, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), sc, base);
+                    fma2(lo, hi, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), by, base);
                     lo = ex2(lo);
                     hi = ex2(hi);
                     add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo, hi);
