@@ -44,14 +44,18 @@ struct Refused {};
     throw Refused{};
 }
 
-const Tensor &cuda_tensor(PyObject *o, const char *name, at::ScalarType type, int index) {
+const Tensor &cuda_tensor(PyObject *o, const char *name, int index) {
     if (!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda())
         refuse(PyExc_TypeError, "%s must be a CUDA tensor", name);
     const Tensor &t = THPVariable_Unpack(o);
-    if (t.scalar_type() != type)
-        refuse(PyExc_TypeError, "%s must be %s, not another type", name, c10::toString(type));
     if (index >= 0 && t.get_device() != index)
         refuse(PyExc_ValueError, "%s must be on the same device as the others%s", name);
+    return t;
+}
+const Tensor &cuda_tensor(PyObject *o, const char *name, at::ScalarType type, int index) {
+    const Tensor &t = cuda_tensor(o, name, index);
+    if (t.scalar_type() != type)
+        refuse(PyExc_TypeError, "%s must be %s, not another type", name, c10::toString(type));
     return t;
 }
 
@@ -292,9 +296,9 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     size_t ws_bytes = 0;
     Tensor captured;   // a captured call's: the graph's pool has it back after this call's launches
     if (a[9] != Py_None) {
-        if (!THPVariable_Check(a[9]) || !THPVariable_Unpack(a[9]).is_cuda())
-            refuse(PyExc_TypeError, "%s must be a CUDA tensor", "workspace");
-        const Tensor &w = THPVariable_Unpack(a[9]);
+        const Tensor &w = cuda_tensor(a[9], "workspace", c.index);
+        if (!w.is_contiguous())
+            refuse(PyExc_ValueError, "%s must be contiguous%s", "workspace");
         ws = w.data_ptr();
         ws_bytes = w.nbytes();
     } else if (need) {
