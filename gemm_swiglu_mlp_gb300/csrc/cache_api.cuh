@@ -404,14 +404,24 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     // a tensor map's strides step over whole rows
     if ((tokens > 1 && q_token_stride < head_dim) || (q_heads > 1 && q_head_stride < head_dim))
         return SWIGLU_ERR_INVALID_ARG;
-    if (tokens > 0) {
-        const size_t obytes = static_cast<size_t>(tokens) * q_heads * head_dim * 2;
-        if (overlaps(out, obytes, q,
-                     rows_extent(tokens, q_heads, head_dim, q_token_stride, q_head_stride)) ||
-            overlaps(out, obytes, k_cache, shape.layer_bytes) ||
-            overlaps(out, obytes, v_cache, shape.layer_bytes))
-            return SWIGLU_ERR_INVALID_ARG;
-    }
+    // what the kernels read while others of their blocks write
+    struct Range { const void *p; size_t n; };
+    const size_t R = static_cast<size_t>(requests), T = static_cast<size_t>(tokens);
+    const size_t obytes = T * static_cast<size_t>(q_heads) * static_cast<size_t>(head_dim) * 2;
+    const Range in[] = {
+        {q, tokens > 0 ? rows_extent(tokens, q_heads, head_dim, q_token_stride, q_head_stride) : 0},
+        {k_cache, shape.layer_bytes},
+        {v_cache, shape.layer_bytes},
+        {block_table, 4 * R * static_cast<size_t>(max_pages)},
+        {ctx_lens, 4 * R},
+        {query_start, 4 * (R + 1)},
+        {mask, 8 * T * static_cast<size_t>(mask_words)}};
+    auto on_input = [&](const void *p, size_t n) {
+        for (const Range &x : in)
+            if (x.p && overlaps(p, n, x.p, x.n)) return true;
+        return false;
+    };
+    if (tokens > 0 && on_input(out, obytes)) return SWIGLU_ERR_INVALID_ARG;
     int dev;
     DeviceState *st;
     const int s = device_setup(&dev, &st);
@@ -422,12 +432,7 @@ int swiglu_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         workspace_bytes < ws.bytes)
         return SWIGLU_ERR_INVALID_ARG;
-    if (overlaps(workspace, ws.bytes, out,
-                 static_cast<size_t>(tokens) * q_heads * head_dim * 2) ||
-        overlaps(workspace, ws.bytes, q,
-                 rows_extent(tokens, q_heads, head_dim, q_token_stride, q_head_stride)) ||
-        overlaps(workspace, ws.bytes, k_cache, shape.layer_bytes) ||
-        overlaps(workspace, ws.bytes, v_cache, shape.layer_bytes))
+    if (overlaps(workspace, ws.bytes, out, obytes) || on_input(workspace, ws.bytes))
         return SWIGLU_ERR_INVALID_ARG;
     TreeAttnArgs a{};
     a.geom.requests = static_cast<int>(requests);

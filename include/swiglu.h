@@ -475,6 +475,7 @@ size_t swiglu_tree_attention_workspace_bytes(int64_t tokens, int64_t q_heads, in
  *             at the same time need their own, and it is not the workspace of
  *             the other entry points (whose counters must stay)
  * Sums and softmax statistics are FP32, the result is rounded once to BF16.
+ * out and the workspace must not overlap each other or an input.
  * query_start must not fall; positions past max_pages * page_size are not
  * seen; a table entry outside the cache is never followed out of it.
  * Errors: SWIGLU_ERR_INVALID_ARG, SWIGLU_ERR_UNSUPPORTED, SWIGLU_ERR_CUDA;
