@@ -69,7 +69,8 @@ def _on(stream, f, *args):
 
 
 class CachePlan(NamedTuple):
-    """What swiglu_cache_plan makes; pass it as `out` to reuse its buffers."""
+    """What swiglu_cache_plan makes; pass it as `out` to reuse its buffers, in
+    turn with another where pages_held and counts[2:3] go into the next step."""
     query_start: torch.Tensor          # [R + 1] int32
     slots: torch.Tensor                # [max_tokens] int32
     positions: torch.Tensor            # [max_tokens] int32
@@ -87,7 +88,11 @@ def swiglu_cache_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, pages_held
     from the requests' lengths, in one launch; nothing is read on the host.
     `max_tokens` rows of slots, positions and masks are made (rows past the
     step's tokens: slot -1, mask 0). `free_head` [1] (None: 0) is where the
-    free list starts; the next step's is counts[2:3]."""
+    free list starts; the next step's is counts[2:3].
+
+    No input may share memory with `out` (SwigluError): every block reads all
+    lengths while others write. So a step that takes the last plan's pages_held or
+    counts[2:3] fills another plan, and two of them alternate."""
     native = _binding or _native()
     if out is None and stream is not None:
         return _on(stream, swiglu_cache_plan, ctx_lens, new_lens, pages_held, block_table,
