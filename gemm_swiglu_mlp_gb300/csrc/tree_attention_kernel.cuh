@@ -1421,21 +1421,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int r0 = tree_min(static_cast<int>(threadIdx.x) * per, g.requests);
     const int r1 = tree_min(r0 + per, g.requests);
     TreeReq q{};
-    int mine[2] = {0, 0};   // units: wide, narrow
-    float cost = 0.f;       // of the wide ones
+    TreeUnits mine{};
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
         q = load(r);
-        const int per_head = tree_head_units(g, q);
-        if (tree_is_narrow(g, q)) {
-            mine[1] += g.kv_heads * per_head;
-        } else {
-            mine[0] += g.kv_heads * per_head;
-            if (per_head) cost += g.kv_heads * tree_wide_cost(g, q, per_head);
-        }
+        tree_add_units(g, q, &mine);
     }
+    float cost = mine.cost;
     // sums up to this thread, in its warp and then over the warps
-    int upto[2] = {mine[0], mine[1]};
+    int upto[2] = {mine.wide, mine.narrow};
     auto warp_scan = [&](int (&v)[2]) {
 #pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
@@ -1477,23 +1471,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (blk.index < (is_narrow ? nb : wb)) {
         blk.cut = is_narrow ? tree_cut(narrow, nb) : tree_cut(wide, wb);
         const int u0 = tree_block_begin(blk.cut, blk.index);
-        const int own = is_narrow ? mine[1] : mine[0];
-        int at = (is_narrow ? upto[1] + (warp ? before_n : 0) : upto[0] + (warp ? before_w : 0)) - own;
-        if (u0 >= at && u0 < at + own) {
-#pragma unroll 1
-            for (int r = r0; r < r1; ++r) {
-                if (per > 1) q = load(r);
-                if (tree_is_narrow(g, q) != is_narrow) continue;
-                const int per_head = tree_head_units(g, q);
-                if (u0 < at + g.kv_heads * per_head) {
-                    start->r = r;
-                    start->units = tree_block_begin(blk.cut, blk.index + 1) - u0;
-                    tree_locate(g, q, u0 - at, per_head, start);
-                    break;
-                }
-                at += g.kv_heads * per_head;
-            }
-        }
+        const int own = is_narrow ? mine.narrow : mine.wide;
+        const int at =
+            (is_narrow ? upto[1] + (warp ? before_n : 0) : upto[0] + (warp ? before_w : 0)) - own;
+        // (a thread of one request has it already)
+        auto again = [&](int r) { return per > 1 ? load(r) : q; };
+        if (u0 >= at && u0 < at + own && tree_find(g, again, is_narrow, r0, r1, at, u0, start))
+            start->units = tree_block_begin(blk.cut, blk.index + 1) - u0;
     }
     // (the sums above have passed block barriers: the address is there)
     blk.tmem = *tmem_holder;

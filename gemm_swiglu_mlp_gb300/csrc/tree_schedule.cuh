@@ -114,6 +114,21 @@ SWIGLU_HD float tree_wide_cost(const TreeGeom &g, const TreeReq &q, int units) {
         cost -= static_cast<float>(tree_item_tiles(g, q, items - 1)) * (kTreePairCost - kTreeOneCost);
     return cost;
 }
+// Both lines' units of some requests, and what the wide ones cost.
+struct TreeUnits {
+    int wide, narrow;
+    float cost;
+};
+SWIGLU_HD void tree_add_units(const TreeGeom &g, const TreeReq &q, TreeUnits *sum) {
+    const int per_head = tree_head_units(g, q);
+    if (tree_is_narrow(g, q)) {
+        sum->narrow += g.kv_heads * per_head;
+    } else {
+        sum->wide += g.kv_heads * per_head;
+        if (per_head) sum->cost += g.kv_heads * tree_wide_cost(g, q, per_head);
+    }
+}
+
 // How many of `blocks` (>= 2 where both lines have work) blocks take the narrow
 // form's line: as its share of the cost.
 SWIGLU_HD int tree_narrow_blocks(int narrow, int wide, float wide_cost, int blocks) {
@@ -164,6 +179,28 @@ SWIGLU_HD void tree_locate(const TreeGeom &g, const TreeReq &q, int rem, int per
     }
     s->item = item;
     s->tile = rem;
+}
+
+// Unit u0 of one form's line, if it falls to one of the requests r0 .. r1 - 1, whose
+// first unit on that line is `at`: sets where it is, and says so.
+template <typename Load>   // Load(r) -> TreeReq
+SWIGLU_HD bool tree_find(const TreeGeom &g, Load load, bool narrow, int r0, int r1, int at, int u0,
+                         TreeStart *s) {
+#ifdef __CUDACC__
+#pragma unroll 1
+#endif
+    for (int r = r0; r < r1; ++r) {
+        const TreeReq q = load(r);
+        if (tree_is_narrow(g, q) != narrow) continue;
+        const int per_head = tree_head_units(g, q);
+        if (u0 < at + g.kv_heads * per_head) {
+            s->r = r;
+            tree_locate(g, q, u0 - at, per_head, s);
+            return true;
+        }
+        at += g.kv_heads * per_head;
+    }
+    return false;
 }
 
 // TreePart::flags
