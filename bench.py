@@ -42,6 +42,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import socket
 import statistics
 import subprocess
@@ -80,10 +81,25 @@ def device_info(dev) -> dict:
             "l2_bytes": getattr(props, "L2_cache_size", None)}
 
 
-def kernel_source_hash() -> str:
+def fused_kernel_sources(csrc: str):
+    """Names of the files that decide what the fused kernels do: their own, what
+    those include, and the host code that chooses and launches them (but not the
+    other kernels that it includes)."""
+    found, todo = set(), ["fused_up_kernel.cuh", "fused_up_pair_kernel.cuh"]
+    while todo:
+        name = todo.pop()
+        if name in found:
+            continue
+        found.add(name)
+        with open(os.path.join(csrc, name)) as f:
+            included = re.findall(r'^#include "([^"]+)"', f.read(), re.M)
+        todo += [n for n in included if os.path.exists(os.path.join(csrc, n))]
+    return sorted(found | {"swiglu_api.cu"})
+
+
+def kernel_source_hash(csrc: str = os.path.join(ROOT, "gemm_swiglu_mlp_gb300", "csrc")) -> str:
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "gemm_swiglu_mlp_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in fused_kernel_sources(csrc):
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()[:16]
