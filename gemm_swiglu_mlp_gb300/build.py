@@ -6,13 +6,15 @@ One translation unit, one -gencode (compute_103a -> sm_103a), static CUDA
 runtime (the library needs no libcudart/libcuda at load time; the driver is
 reached through cudaGetDriverEntryPointByVersion when a call needs it). Beside
 it the binding module of the paged-cache calls, host C++ against the installed
-PyTorch (its version is in the file's name).
+PyTorch (its version is in the file's name). It is left out, with a note, where
+the headers for it are missing: the library and its C ABI do not need them.
 """
 from __future__ import annotations
 
 import importlib.metadata
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -25,8 +27,17 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libswiglu_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 BINDING_SOURCE = os.path.join(CSRC, "cache_binding.cpp")
+
+
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "none"
+
+
 BINDING_PATH = os.path.join(PKG_DIR, "_cache_binding_%s.so" % "".join(
-    c if c.isalnum() else "_" for c in importlib.metadata.version("torch")))
+    c if c.isalnum() else "_" for c in _torch_version()))
 SOURCES = [os.path.join(CSRC, "swiglu_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(INCLUDE, "swiglu.h")]
@@ -66,11 +77,32 @@ def up_to_date() -> bool:
     return _newer(LIB_PATH, DEPS)
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else ""
+
+
+def _cuda_dir() -> str:
+    return os.path.dirname(os.path.dirname(nvcc_path())) or "/usr/local/cuda"
+
+
+def binding_needs():
+    """What the binding module's build needs and does not find: names, for people."""
+    inc = os.path.join(_torch_dir(), "include")
+    needs = [("g++", shutil.which("g++")),
+             ("Python's headers", os.path.exists(
+                 os.path.join(sysconfig.get_paths()["include"], "Python.h"))),
+             ("PyTorch with its headers", _torch_dir() and os.path.exists(
+                 os.path.join(inc, "torch", "csrc", "autograd", "python_variable.h"))),
+             ("the CUDA toolkit's headers", os.path.exists(
+                 os.path.join(_cuda_dir(), "include", "cuda_runtime_api.h")))]
+    return [name for name, found in needs if not found]
+
+
 def binding_command(out_path: str):
     """g++ on the binding module, with the installed PyTorch's headers and libraries."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch_dir, cuda = _torch_dir(), _cuda_dir()
     inc = os.path.join(torch_dir, "include")
-    cuda = os.path.dirname(os.path.dirname(nvcc_path())) or "/usr/local/cuda"
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + INCLUDE, "-I" + inc,
             "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
             "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
@@ -91,7 +123,13 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Both, at the same time; returns the library's path."""
+    """Both, at the same time; returns the library's path. An error in either is
+    raised; headers that the binding needs and that are not there only leave it out."""
+    missing = binding_needs()
+    if missing:
+        sys.stderr.write("%s is left out (the paged-cache calls from Python need it): no %s\n"
+                         % (os.path.basename(BINDING_PATH), ", no ".join(missing)))
+        return build_library(force, verbose)
     errors = []
 
     def binding():

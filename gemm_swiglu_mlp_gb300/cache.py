@@ -28,7 +28,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import SwigluError, load_library
-from .build import BINDING_PATH
+from .build import BINDING_PATH, binding_needs
 
 _binding = None
 
@@ -40,8 +40,10 @@ def _native():
     if _binding is None:
         lib = load_library()
         if not os.path.exists(BINDING_PATH):
-            raise RuntimeError("%s is not built; run `python -m gemm_swiglu_mlp_gb300.build`"
-                               % os.path.basename(BINDING_PATH))
+            missing = binding_needs()
+            raise RuntimeError("%s is not built%s; run `python -m gemm_swiglu_mlp_gb300.build`"
+                               % (os.path.basename(BINDING_PATH),
+                                  " (it needs %s)" % ", ".join(missing) if missing else ""))
         loader = importlib.machinery.ExtensionFileLoader("_cache_binding", BINDING_PATH)
         spec = importlib.util.spec_from_file_location("_cache_binding", BINDING_PATH, loader=loader)
         mod = importlib.util.module_from_spec(spec)
