@@ -1,11 +1,12 @@
 // The Python side of the paged-cache entry points (include/swiglu.h), natively:
 // argument checks, device and stream, output buffers and the C ABI call.
 //
-// These calls are 2 to 12 microseconds of GPU time in a serving step, several a
-// layer. Checked and marshalled in Python they took 11 to 18 microseconds of
-// the host's, so a step waited for its host; here the whole way is about one
-// microsecond plus the launches. The module holds no operator: it calls the
-// functions of libswiglu_gb300.so, whose addresses cache.py gives it.
+// Small ones of these calls take 2 to 16 microseconds of GPU time in a serving step,
+// several a layer. Checked and marshalled in Python they took the host 10.6 (plan),
+// 7.4 (write), 13 (accept) and 18 (attention, which is two launches), so a step
+// waited for its host; here they take 2.8, 2.0, 3.8 and 10.3, launches included.
+// The module holds no operator: it calls the functions of libswiglu_gb300.so,
+// whose addresses cache.py gives it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -5,7 +5,7 @@
 //
 // Cache: K and V each [pages][kv heads][page rows][head size] BF16, so one
 // page of one head is a contiguous block (4 KB at 16 rows of 128) that the
-// attention kernel fetches with one tensor-map box per 64 columns. Position
+// attention kernel fetches as one 5-D tensor-map box. Position
 // x of request r is row x % P of page table[r][x / P]; its slot is
 // page * P + x % P.
 #pragma once
@@ -62,7 +62,7 @@ __device__ __forceinline__ int plan_wanted(const CachePlanArgs &a, int r, int n,
 // launch or a wait between blocks. Then tokens are spread over all threads of
 // the grid and requests' new pages over its warps. A chain of dependent loads
 // bounds it (lengths, the request's table, the parents up a tree), not the bytes:
-// 64 requests of one token 3.4 us, 192 trees of up to 60 tokens 5.2, of which an
+// 64 requests of one token 3.5 us, 192 trees of up to 60 tokens 5.3, of which an
 // empty launch is 2.
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePlanArgs a) {
     extern __shared__ int plan_smem[];
@@ -207,7 +207,7 @@ struct CacheWriteArgs {
 // One 16-byte chunk of K and the same one of V a thread: both loads are in
 // flight before either store; consecutive threads take consecutive chunks of
 // a row on both sides (128 or 256 contiguous bytes). Its bytes bound it: 10
-// prompts of up to 2000 tokens, 8 kv heads of 128, 22.4 us, 6.3 TB/s read and
+// prompts of up to 2000 tokens, 8 kv heads of 128, 22.6 us, 6.2 TB/s read and
 // written; small calls are an empty launch's 2 us.
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheWriteArgs a) {
     griddep_launch_dependents();
@@ -253,7 +253,7 @@ struct CacheAcceptArgs {
 // path[j] >= j > i for j > i: no row is written before it has been read,
 // neither within a batch (all of its loads come first) nor by an earlier one.
 // The addresses (path, then table, then rows) are its time, not the bytes: one
-// layer of 8 requests 2.2 us, 28 layers of 48 requests 4.3.
+// layer of 8 requests 2.3 us, 28 layers of 48 requests 3.5.
 __global__ void __launch_bounds__(kAcceptThreads) cache_accept_kernel(const CacheAcceptArgs a) {
     __shared__ long long src[32], dst[32];   // chunk offsets at head 0 of a layer
     __shared__ int moves;

@@ -6,8 +6,13 @@
 // (x < c) and, of the step's own tokens (x = c + j), those whose bit j is set
 // in the token's mask words (without a mask: j <= t's own place). A row that
 // sees nothing, or only scores of -inf, is zero. Scores, sums and statistics
-// are FP32; the weights p are rounded to BF16 for the second product (the
-// tensor cores take BF16 pairs), the result once to BF16.
+// are FP32; the weights p are rounded to BF16 for the second product (the tensor
+// cores take both operands in one type, and V is BF16), the result once to BF16: 0.0019 to
+// 0.0023 of the values' deviation off 64-bit results, where FP32 weights would
+// be 0.0016 to 0.0017 off. The sum below the line is of the rounded weights in the
+// narrow form, where it is a product too, and of the unrounded ones in the wide
+// form, where it is taken before they are rounded; roundings to nearest average
+// out in either.
 //
 // One persistent block per SM works through its share of the line of tiles
 // (tree_schedule.cuh). All query heads of a kv head and many tokens fill the
@@ -51,12 +56,14 @@
 // requests of one token, contexts of 4000, 4 kv heads of 128: 5.6 TB/s of
 // K and V over the whole call, pages of 64 rows). Wide, two row tiles an item:
 // the chain of one tile - scores 512 clocks of the tensor cores, softmax 1900,
-// result 512, and some 1000 of waits, barriers and issue between them - which
-// two groups can only half overlap, as TMEM holds no third tile's scores (32
-// requests of up to 64 tokens, 8 heads a kv head, contexts of 2000 to 6000:
-// 268 us, 742 TFLOP/s of products that count). No single piece of it is the
-// bound: without the exponentials, or half of either product, it takes 4%
-// less. Small calls: 6 us are launch, the shares' prologue and the end of the
+// result 512, and some 1000 of waits, barriers and issue between them. While one
+// group is in its softmax, the tensor cores have the other group's products to do,
+// 1024 clocks, and then wait for it: two tiles of scores would keep them busy if the
+// softmax were no longer than that (32 requests of up to 64 tokens, 8 heads a kv
+// head, contexts of 2000 to 6000: 271 us, 732 TFLOP/s of products that count).
+// No single piece of it is the bound: without the exponentials, or half of either
+// product, it takes 4% less. At its 96 registers the kernel spills a little (92 bytes
+// of stores and 184 of loads at head size 128, 104 and 196 at 64). Small calls: 6 us are launch, the shares' prologue and the end of the
 // kernel, 2 to 3 the join.
 //
 // Five roles run different code at once, and the SM's instruction cache holds

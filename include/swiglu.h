@@ -389,7 +389,8 @@ int swiglu_mlp_forward(const void *A, const void *Wpacked, const void *W3packed,
  * page_size + row is its slot. page_size is 16, 32, 64 or 128, head_dim 64 or
  * 128, num_pages * page_size < 2^31 (other values: SWIGLU_ERR_UNSUPPORTED).
  * All index arrays are device int32; nothing is read on the host, so every
- * call may be captured into a CUDA graph and replayed with other lengths.
+ * call may be captured into a CUDA graph and replayed with other lengths (a
+ * workspace then has to stay allocated as long as the graph).
  *
  *     swiglu_cache_plan       lengths (and trees) -> pages, slots, masks
  *     swiglu_cache_write      new K and V rows into the cache, by slot
@@ -474,7 +475,9 @@ size_t swiglu_tree_attention_workspace_bytes(int64_t tokens, int64_t q_heads, in
  *             aligned, any content; every call overwrites it, so calls that run
  *             at the same time need their own, and it is not the workspace of
  *             the other entry points (whose counters must stay)
- * Sums and softmax statistics are FP32, the result is rounded once to BF16.
+ * Scores, sums and softmax statistics are FP32; the weights p are rounded to BF16
+ * before they multiply the values, and the result once to BF16. Scores may be of
+ * any finite size.
  * out and the workspace must not overlap each other or an input.
  * query_start must not fall; positions past max_pages * page_size are not
  * seen; a table entry outside the cache is never followed out of it.
