@@ -168,13 +168,18 @@ struct VerifyLeft {
         e = some ? e : 0.f;
     }
     __device__ __forceinline__ int draft() const { return !q ? 0 : S == 1.f && S_low == 0.f ? 1 : 2; }
-    __device__ __forceinline__ unsigned long long at(float pv, float qv) const {
+    // (with q or without)
+    __device__ __forceinline__ float2 both(float pv, float qv) const {
         float w, e;
         if (q)
             pair<2>(pv, qv, w, e);
         else
             pair<0>(pv, qv, w, e);
-        return verify_units(w, e);
+        return make_float2(w, e);
+    }
+    __device__ __forceinline__ unsigned long long at(float pv, float qv) const {
+        const float2 w = both(pv, qv);
+        return verify_units(w.x, w.y);
     }
 };
 
@@ -230,14 +235,32 @@ __device__ __forceinline__ unsigned long long verify_range(const VerifyLeft<T> &
     return sum.units();
 }
 
-// What is left at value i < hi (0 past it, and at the `skips` values of skip).
+// What is left at value i < hi (0 past it, and at the `skips` values of skip), as a pair.
+template <typename T>
+__device__ __forceinline__ float2 verify_pair(const VerifyLeft<T> &left, int i, int hi, const int *skip,
+                                              int skips) {
+    if (i >= hi) return make_float2(0.f, 0.f);
+    for (int j = 0; j < skips; ++j)
+        if (skip[j] == i) return make_float2(0.f, 0.f);
+    return left.both(verify_load(left.p + i), left.q ? verify_load(left.q + i) : 0.f);
+}
 template <typename T>
 __device__ __forceinline__ unsigned long long verify_value(const VerifyLeft<T> &left, int i, int hi,
                                                            const int *skip, int skips) {
-    if (i >= hi) return 0;
-    for (int j = 0; j < skips; ++j)
-        if (skip[j] == i) return 0;
-    return left.at(verify_load(left.p + i), left.q ? verify_load(left.q + i) : 0.f);
+    const float2 w = verify_pair(left, i, hi, skip, skips);
+    return verify_units(w.x, w.y);
+}
+
+// The first value of [lo, hi) of which anything is left, or -1. All 32 lanes.
+template <typename T>
+__device__ __noinline__ int verify_first(const VerifyLeft<T> &left, int lo, int hi, const int *skip,
+                                         int skips, int lane) {
+    for (int base = lo; base < hi; base += 32) {
+        const float w = verify_pair(left, base + lane, hi, skip, skips).x;
+        const unsigned some = __ballot_sync(~0u, w > 0.f);
+        if (some) return base + __ffs(some) - 1;
+    }
+    return -1;
 }
 
 // What warp 0 wants of its CTA's warps.
@@ -482,6 +505,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
                 if (want < all) found = base + verify_pick(w, &want, lane);
                 else want -= all;
             }
+            // None of the piece's values counts by itself (all of them are below 2^-51), though the
+            // lanes' sums of them do: the first that is not 0.
+            if (sub < 0) found = verify_first(left, b0, min(b0 + piece, a.vocab), skip, skips, lane);
         }
     }
     command(left, -2, 0);
