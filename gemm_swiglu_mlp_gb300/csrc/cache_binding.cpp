@@ -11,7 +11,9 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -483,15 +485,13 @@ const Tensor &probabilities(PyObject *o, const char *name, at::ScalarType type, 
 // (a single row's stride may be anything)
 int64_t row_stride(const Tensor &t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
 
-// A contiguous tensor in the memory of another, from its element `offset` on: a call's new
-// outputs share one allocation, as three take the host longer than the rest of the call (a
-// greedy one 6.2 us, with one 4.9).
-Tensor within(const Tensor &whole, at::IntArrayRef sizes, int64_t offset) {
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()),
-                                                        whole.key_set(), whole.dtype());
-    t.unsafeGetTensorImpl()->set_storage_offset(offset);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-    return t;
+// A new contiguous int32 tensor on the current device, in memory of its own (so that a caller may
+// resize it), straight from the allocator: a greedy verification with three of them takes the
+// host 4.7 us, and 6.2 with three through the dispatcher.
+Tensor new_i32(at::IntArrayRef sizes) {
+    return Tensor(at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(),
+                                            c10::DispatchKeySet(c10::DispatchKey::CUDA), at::kInt,
+                                            std::nullopt));
 }
 
 // verify(tokens, query_start, target, parents, draft, uniform, width, paths, path_lens,
@@ -546,18 +546,12 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
         uniform = &u;
     }
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-    Tensor made[3], all;
-    if (a[7] == Py_None && a[8] == Py_None && a[9] == Py_None)
-        all = at::empty({R * (width + 2)}, tokens.options());
+    Tensor made[3];
     void *out[3];
     static const char *const names[3] = {"out.paths", "out.path_lens", "out.next_tokens"};
     for (int i = 0; i < 3; ++i) {
         if (a[7 + i] == Py_None) {
-            if (all.defined())
-                made[i] = i ? within(all, {R}, R * (width + i - 1)) : within(all, {R, width}, 0);
-            else
-                made[i] = i ? at::empty({R}, tokens.options())
-                            : at::empty({R, width}, tokens.options());
+            made[i] = i ? new_i32({R}) : new_i32({R, width});
             out[i] = made[i].data_ptr();
             continue;
         }
