@@ -174,6 +174,19 @@ bool verify_setup() {
     return verify_setup_one<float, true>() && verify_setup_one<float, false>() &&
            verify_setup_one<__nv_bfloat16, true>() && verify_setup_one<__nv_bfloat16, false>();
 }
+// device_setup and, with that device's first verification of probabilities, its own.
+int verify_device(DeviceState **st) {
+    int dev;
+    const int s = device_setup(&dev, st);
+    if (s != SWIGLU_OK) return s;
+    DeviceState &d = **st;
+    std::call_once(d.verify_once, [&d] {
+        if (verify_setup()) return;
+        cudaGetLastError();
+        d.verify_status = SWIGLU_ERR_CUDA;
+    });
+    return d.verify_status;
+}
 
 // One 4-bit product: out [M, N] from A [M, K], or the gated form with Q2 and S2.
 struct Q4Problem {
@@ -343,24 +356,6 @@ int q4_forward(const Q4Problem &p, const DeviceState &st, void *stream) {
         return q4_launch<decltype(c)::nt, GATED, decltype(c)::groups>(p, st, stream);
     });
 }
-// Workspace of one product on the current device.
-template <bool GATED>
-size_t q4_workspace(int64_t M, int64_t N, int64_t K, int64_t group) {
-    if (M < 1 || M > (1 << 20) || N < 8 || K < 32 || N >= kMaxI32 || K >= kMaxI32 ||
-        (group != 32 && group != 64 && group != 128))
-        return 0;
-    int dev;
-    DeviceState *st;
-    if (device_setup(&dev, &st) != SWIGLU_OK) return 0;
-    Q4Problem p{};
-    p.M = M;
-    p.N = N;
-    p.K = K;
-    p.group = group;
-    return q4_choose(M, group, [&](auto c) {
-        return q4_plan<decltype(c)::nt, GATED, decltype(c)::groups>(p, *st).workspace;
-    });
-}
 
 // Once a device: the kernels' shared memory and cluster sizes, and how many clusters of j CTAs
 // run at once, two CTAs an SM (16 tokens' kernel) or one (32 tokens').
@@ -402,10 +397,41 @@ bool q4_setup_rows(int sms, int *clusters) {
     }
     return true;
 }
-bool q4_setup(DeviceState &st, int sms) {
+bool q4_setup(DeviceState &st) {
     return q4_setup_one<1, true, 1>() && q4_setup_one<1, false, 1>() &&
-           q4_setup_rows<1>(sms, nullptr) && q4_setup_rows<2>(sms, st.q4_clusters_2) &&
-           q4_setup_rows<4>(sms, st.q4_clusters_1);
+           q4_setup_rows<1>(st.sm_count, nullptr) && q4_setup_rows<2>(st.sm_count, st.q4_clusters_2) &&
+           q4_setup_rows<4>(st.sm_count, st.q4_clusters_1);
+}
+// device_setup and, with that device's first 4-bit product (or its workspace's size), its own.
+int q4_device(DeviceState **st) {
+    int dev;
+    const int s = device_setup(&dev, st);
+    if (s != SWIGLU_OK) return s;
+    DeviceState &d = **st;
+    std::call_once(d.q4_once, [&d] {
+        if (q4_setup(d)) return;
+        cudaGetLastError();
+        d.q4_status = SWIGLU_ERR_CUDA;
+    });
+    return d.q4_status;
+}
+
+// Workspace of one product on the current device.
+template <bool GATED>
+size_t q4_workspace(int64_t M, int64_t N, int64_t K, int64_t group) {
+    if (M < 1 || M > (1 << 20) || N < 8 || K < 32 || N >= kMaxI32 || K >= kMaxI32 ||
+        (group != 32 && group != 64 && group != 128))
+        return 0;
+    DeviceState *st;
+    if (q4_device(&st) != SWIGLU_OK) return 0;
+    Q4Problem p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.group = group;
+    return q4_choose(M, group, [&](auto c) {
+        return q4_plan<decltype(c)::nt, GATED, decltype(c)::groups>(p, *st).workspace;
+    });
 }
 
 }  // namespace
@@ -485,7 +511,7 @@ int swiglu_verify_drafts(const int32_t *tokens, int64_t rows, const int32_t *que
         if (overlaps_any(out[i], in, 6) || overlaps_any(out[i], out, i)) return SWIGLU_ERR_INVALID_ARG;
     int dev;
     DeviceState *st;
-    const int s = device_setup(&dev, &st);
+    const int s = greedy ? device_setup(&dev, &st) : verify_device(&st);
     if (s != SWIGLU_OK) return s;
     if (requests == 0) return SWIGLU_OK;
     VerifyArgs a{};
@@ -562,10 +588,9 @@ int swiglu_up_forward_q4(const void *A, const void *Q1, const void *S1, const vo
                          const void *S2, void *Y, int64_t M, int64_t N, int64_t K, int64_t group,
                          void *workspace, size_t workspace_bytes, void *stream) {
     const Q4Problem up{A, Q1, S1, Q2, S2, Y, M, N, K, group, workspace, workspace_bytes};
-    int dev;
     DeviceState *st;
     int s = q4_check(up, true);
-    if (s == SWIGLU_OK) s = device_setup(&dev, &st);
+    if (s == SWIGLU_OK) s = q4_device(&st);
     return s == SWIGLU_OK ? q4_forward<true>(up, *st, stream) : s;
 }
 
@@ -574,10 +599,9 @@ int swiglu_down_forward_q4(const void *Y, const void *Q3, const void *S3, void *
                            size_t workspace_bytes, void *stream) {
     const Q4Problem down{Y, Q3, S3, nullptr, nullptr, out, M, K, N, group, workspace,
                          workspace_bytes};
-    int dev;
     DeviceState *st;
     int s = q4_check(down, false);
-    if (s == SWIGLU_OK) s = device_setup(&dev, &st);
+    if (s == SWIGLU_OK) s = q4_device(&st);
     return s == SWIGLU_OK ? q4_forward<false>(down, *st, stream) : s;
 }
 
@@ -599,9 +623,8 @@ int swiglu_mlp_forward_q4(const void *A, const void *Q1, const void *S1, const v
     if (overlaps_any({out, static_cast<size_t>(M) * static_cast<size_t>(K) * 2}, of_up, 5) ||
         overlaps_any({Y, static_cast<size_t>(M) * static_cast<size_t>(N) * 2}, of_down, 2))
         return SWIGLU_ERR_INVALID_ARG;
-    int dev;
     DeviceState *st;
-    s = device_setup(&dev, &st);
+    s = q4_device(&st);
     if (s == SWIGLU_OK) s = q4_forward<true>(up, *st, stream);
     return s == SWIGLU_OK ? q4_forward<false>(down, *st, stream) : s;
 }

@@ -66,7 +66,11 @@ struct DeviceState {
     // clusters of j CTAs of the decode down-projection kernel that can run at
     // once, j = 1..kDecodeMaxSplits (0: that size cannot be launched)
     int decode_clusters[kDecodeMaxSplits + 1] = {};
-    // the same of the 4-bit kernels, one and two CTAs an SM
+    // Draft verification and the 4-bit products have a setup of their own (step_api.cuh), at the
+    // first of their calls: the others neither wait for it nor fail with it.
+    std::once_flag verify_once, q4_once;
+    int verify_status = SWIGLU_OK, q4_status = SWIGLU_OK;
+    // clusters of j CTAs of the 4-bit kernels at once, one and two CTAs an SM
     int q4_clusters_1[kQ4MaxSplits + 1] = {}, q4_clusters_2[kQ4MaxSplits + 1] = {};
 };
 
@@ -90,9 +94,6 @@ EncodeTiledFn get_encode() {
     });
     return g_encode;
 }
-
-bool verify_setup();   // these two: step_api.cuh
-bool q4_setup(DeviceState &st, int sms);
 
 // One-time per-device setup with that device current: check that it is an
 // sm_103 part, cache its SM count and raise the kernel's shared-memory limit.
@@ -179,9 +180,7 @@ int device_setup(int *dev_out, DeviceState **st_out) {
             cudaFuncSetAttribute(tree_attention_kernel<128>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  TreeShared<128>::SMEM_BYTES) != cudaSuccess ||
-            !verify_setup() ||
-            !q4_setup(st, sms) ||
-            // the decode kernel's clusters of up to 16 CTAs (more than the portable 8)
+            // its clusters of up to 16 CTAs (more than the portable 8)
             cudaFuncSetAttribute(down_decode_kernel<32>,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
             cudaFuncSetAttribute(down_decode_kernel<64>,
