@@ -162,17 +162,40 @@ int head_rotate(const Heads &q, const Heads &k, const int32_t *positions, int64_
     return launch_overlapped(kernel, dim3(static_cast<unsigned>(blocks)), kRotateThreads, 0, stream, a);
 }
 
-// Once a device: the widest tree's shared memory, and clusters of more than the portable 8.
+// Once a device: the widest tree's shared memory, clusters of more than the portable 8, and the
+// largest cluster (a power of two) of which one can run with that much of it: *fits at most.
 template <typename T, bool VEC>
-bool verify_setup_one() {
-    return cudaFuncSetAttribute(verify_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                6 * 4 * kVerifyMaxWidth) == cudaSuccess &&
-           cudaFuncSetAttribute(verify_kernel<T, VEC>,
-                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+bool verify_setup_one(int *fits) {
+    auto kernel = verify_kernel<T, VEC>;
+    constexpr int bytes = 6 * 4 * kVerifyMaxWidth;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    for (; *fits > 1; *fits /= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(*fits);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(*fits));
+        cfg.blockDim = dim3(kVerifyThreads);
+        cfg.dynamicSmemBytes = bytes;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0)
+            break;
+        cudaGetLastError();
+    }
+    return true;
 }
-bool verify_setup() {
-    return verify_setup_one<float, true>() && verify_setup_one<float, false>() &&
-           verify_setup_one<__nv_bfloat16, true>() && verify_setup_one<__nv_bfloat16, false>();
+bool verify_setup(DeviceState &st) {
+    st.verify_cluster = kVerifyMaxCluster;
+    int *fits = &st.verify_cluster;
+    return verify_setup_one<float, true>(fits) && verify_setup_one<float, false>(fits) &&
+           verify_setup_one<__nv_bfloat16, true>(fits) && verify_setup_one<__nv_bfloat16, false>(fits);
 }
 // device_setup and, with that device's first verification of probabilities, its own.
 int verify_device(DeviceState **st) {
@@ -181,7 +204,7 @@ int verify_device(DeviceState **st) {
     if (s != SWIGLU_OK) return s;
     DeviceState &d = **st;
     std::call_once(d.verify_once, [&d] {
-        if (verify_setup()) return;
+        if (verify_setup(d)) return;
         cudaGetLastError();
         d.verify_status = SWIGLU_ERR_CUDA;
     });
@@ -540,12 +563,7 @@ int swiglu_verify_drafts(const int32_t *tokens, int64_t rows, const int32_t *que
     const uintptr_t vec = 4 * size - 1;
     const bool by_four = ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) &
                           vec) == 0 && target_stride % 4 == 0 && draft_stride % 4 == 0;
-    // CTAs a request: about two an SM over all requests, none with less than a load a lane (one
-    // request of 152000 values: 8.5 us with 16; 64 requests of 128000 17.5 with 4)
-    int ctas = 1;
-    while (ctas < kVerifyMaxCluster && 2 * ctas * requests <= 2 * st->sm_count &&
-           2 * ctas * kVerifyThreads * 4 <= vocab)
-        ctas *= 2;
+    const int ctas = verify_ctas(requests, vocab, st->sm_count, st->verify_cluster);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -70,6 +70,7 @@ struct DeviceState {
     // first of their calls: the others neither wait for it nor fail with it.
     std::once_flag verify_once, q4_once;
     int verify_status = SWIGLU_OK, q4_status = SWIGLU_OK;
+    int verify_cluster = 1;  // CTAs of the verification's largest cluster that can run
     // clusters of j CTAs of the 4-bit kernels at once, one and two CTAs an SM
     int q4_clusters_1[kQ4MaxSplits + 1] = {}, q4_clusters_2[kQ4MaxSplits + 1] = {};
 };

@@ -33,13 +33,12 @@
 #include <cuda_bf16.h>
 
 #include "epilogue.cuh"
+#include "verify_split.cuh"
 
 namespace swiglu {
 
-constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyMaxWidth = 4096;    // tokens a request: the tree lies in shared memory
-constexpr int kVerifyMaxCluster = 16;    // CTAs a request
 constexpr int kVerifyMaxVocab = 1 << 20;
 constexpr int kVerifyUnroll = 4;         // loads of p (and q) a lane has in flight, 4 values each
 
