@@ -132,8 +132,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 //   up to 8 (instructions issued): they are used as they are. The tokens are multiplied by 2^60,
 //   or 2^56 where they meet sixteens, which takes the products into FP32's range, and a
 //   group's sums start from -8 times the tokens' sum: a multiply-add less for every code
-//   pair, 4 matrix instructions more for 16 (one token, 2 weights of 3584 x 18944, when it was
-//   tried: 15.2 -> 14.2 us; 16 tokens, 2 of 8192 x 29568: 69 us, but 73 this way).
+//   pair, 4 matrix instructions more for 16 (one token, 2 weights of 3584 x 18944: 15.0 -> 14.3 us,
+//   of 8192 x 29568 52.3 -> 47.1; 16 tokens, 2 of 8192 x 29568: 69 us, but 73 this way).
+//   All sums are 2^-73 of what they stand for then, so FP32's smallest step is 2^-76 of it, and
+//   values from 2^68 on pass FP32's range: the contract says so. (Scales times 2^57 would leave
+//   that step to a group's sums only; it is an instruction for every two scales, 14.25 -> 14.40 us,
+//   5 tokens of 4864 x 896 with groups of 32 4.23 -> 4.46.)
 template <int NT>
 struct Q4Form {
     static constexpr bool DIRECT = NT == 1;

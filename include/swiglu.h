@@ -633,8 +633,15 @@ int swiglu_verify_drafts(const int32_t *tokens, int64_t rows, const int32_t *que
  * [ceil(K / group), N]; group 32, 64 or 128. They are read as they lie: nothing is
  * packed. Products and sums are FP32 (codes are exact, scales multiply a group's sum),
  * each output is rounded once to BF16; the same from run to run. With up to 8 rows a
- * product's A (or Y) has to be below 2^67 in magnitude (others count as infinite), and a
- * group is summed as sum(code * a) - 8 sum(a).
+ * group is summed as sum(code * a) - 8 sum(a), so that
+ *   - codes that are all 8 come to 0 within the rounding of those sums only;
+ *   - a product's A (or Y) has to be below 2^67 in magnitude: its row is NaN if it has an
+ *     infinite value, and may be if it has any other that large;
+ *   - sums are held in steps of 2^-76: a group's before its scale, and the result. Rows whose
+ *     values are all below about 2^-60, and results below about 2^-66, are less accurate
+ *     than BF16.
+ * With more rows none of this holds; a row's result may differ in its last bit by the
+ * number of rows.
  *
  *   swiglu_up_forward_q4    Y [M, N] = SiLU(A W1^T) (.) (A W2^T), A [M, K]
  *   swiglu_down_forward_q4  out [M, K] = Y W3^T, Y [M, N]; codes Q3 [K, N / 2], scales S3
