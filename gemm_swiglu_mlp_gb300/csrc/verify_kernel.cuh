@@ -16,10 +16,13 @@
 // several refusals is max(p - S q, 0) with S the sum of the Zs so far: one row of p
 // and one of q are all there is to read, whatever the number of children.
 //
-// Sums and borders are held to about 2^-50, in whole units of it between warps:
-// with 32-bit sums (2^-24) one draw in some hundreds would give a neighbour of the token.
-// A lane adds its values up as pairs of FP32 numbers, each addition's error
-// kept: conversions of every value to a 64-bit integer, which go at a rate of two a clock and
+// Sums are whole units of 2^-50 between lanes: with 32-bit sums (2^-24) one draw in
+// some hundreds would give a neighbour of the token. A lane adds its values up as pairs of FP32
+// numbers, each addition's error kept. The pairs' second numbers are rounded: at most 2^-43 of
+// the lane's sum for 16 values between two settlings, 2^-36 for the 2048 values that a
+// lane has of 2^20 over one CTA, and the lanes' own units 2^-37 and the draw's 2^-38 more, so
+// that a row's borders are held to 2^-35; rows of a softmax to about 2^-44, as roundings go
+// both ways (of a value .55 and 2^20 equal ones 2^-31 without settling). Conversions of every value to a 64-bit integer, which go at a rate of two a clock and
 // SM, were most of the time of a batch (64 rows of 128000 52 us), and digits taken
 // off by additions of constants half as many instructions again as the pairs.
 //
@@ -142,6 +145,13 @@ struct VerifySum {
         s = t;
         c = __fadd_rn(c, __fadd_rn(err, e));
     }
+    // The pair with s as near to the sum as it gets, so that c is small and its own additions lose
+    // less: over n values without it c grows by n half steps of s and loses n^2 2^-50.
+    __device__ __forceinline__ void settle() {
+        const float t = __fadd_rn(s, c);
+        c = __fsub_rn(c, __fsub_rn(t, s));
+        s = t;
+    }
     __device__ __forceinline__ unsigned long long units() const { return verify_units(s, c); }
 };
 
@@ -230,6 +240,7 @@ __device__ __forceinline__ unsigned long long verify_range(const VerifyLeft<T> &
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum.add(w[i], e[i]);
         }
+        sum.settle();
     }
     return sum.units();
 }
