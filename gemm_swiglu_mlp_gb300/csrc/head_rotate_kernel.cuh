@@ -9,7 +9,8 @@
 // FP32 throughout, one rounding to BF16 at the end. The angle is reduced to a
 // part of a turn in 64-bit fixed point, where whole turns fall off the top of a
 // wrapping product: position * (inv_freq / 2 pi * 2^64). In FP32 the product
-// alone would be off by 2^-24 of itself, 0.06 radians at position 1000000.
+// alone would be off by 2^-24 of itself, 0.06 radians at position 1000000. The part of a turn
+// that is left, in units of 2^-32, is rounded to FP32 (2^-26 turns) for its sine and cosine.
 #pragma once
 
 #include <cuda_bf16.h>

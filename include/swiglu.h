@@ -530,7 +530,9 @@ int swiglu_cache_accept(void *k_cache, void *v_cache, int64_t layers, int64_t nu
  *     (y1, y2) -> (y1 cos a_i - y2 sin a_i, y1 sin a_i + y2 cos a_i)
  * with (y1, y2) = (y[i], y[i + freqs]), or (y[2i], y[2i + 1]) if interleaved is
  * not 0. Values behind them are only normed. FP32 throughout and one rounding
- * to BF16; the angle is exact to 2^-32 turns at any position.
+ * to BF16: a head whose squares sum to more than FP32 holds comes out as 0, and with eps = 0
+ * one whose squares all vanish in it (below 2^-149) is not finite. The angle is held to
+ * 2^-26 turns (a rounding to FP32) and |inv_freq * position| * 2^-64, at any position.
  *   q, k       device BF16, strides in elements (multiples of 8; the last dimension
  *              contiguous; 16-byte aligned), e.g. slices of a fused projection's output
  *   positions  device int32 [tokens] (any value)
