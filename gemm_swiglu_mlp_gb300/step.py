@@ -59,7 +59,8 @@ def swiglu_head_rotate_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 
 class Verified(NamedTuple):
-    """What swiglu_verify_drafts finds; pass it as `out` to reuse its buffers."""
+    """What swiglu_verify_drafts finds; pass it as `out` to reuse its buffers (None in one's
+    place: a new one)."""
     paths: torch.Tensor          # [R, width] int32: places of the tokens that hold, then -1
     path_lens: torch.Tensor      # [R] int32
     next_tokens: torch.Tensor    # [R] int32: the token that follows
@@ -77,11 +78,11 @@ def swiglu_verify_drafts(tokens: torch.Tensor, query_start: torch.Tensor, target
     `parents` [R, width] as for swiglu_cache_plan; chains (None) need `width`, the most
     tokens a request has."""
     f = (cache._binding or _native()).verify
-    if out is None and stream is not None:
+    given = (None, None, None) if out is None else tuple(out)
+    if stream is not None and any(t is None for t in given):
         return Verified(*_on(stream, f, tokens, query_start, target, parents, draft, uniform, width,
-                             None, None, None, None))
-    return Verified(*f(tokens, query_start, target, parents, draft, uniform, width,
-                       *(out or (None, None, None)), stream))
+                             *given, None))
+    return Verified(*f(tokens, query_start, target, parents, draft, uniform, width, *given, stream))
 
 
 def swiglu_up_q4_workspace_bytes(M: int, N: int, K: int, group: int = 128) -> int:
