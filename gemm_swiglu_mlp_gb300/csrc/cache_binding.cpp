@@ -487,7 +487,7 @@ int64_t row_stride(const Tensor &t) { return t.size(0) > 1 ? t.stride(0) : t.siz
 
 // A new contiguous int32 tensor on the current device, in memory of its own (so that a caller may
 // resize it), straight from the allocator: a greedy verification with three of them takes the
-// host 4.7 us, and 6.2 with three through the dispatcher.
+// host 4.7 to 5.1 us, with one allocation cut into three 4.5 to 5.5.
 Tensor new_i32(at::IntArrayRef sizes) {
     return Tensor(at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(),
                                             c10::DispatchKeySet(c10::DispatchKey::CUDA), at::kInt,

@@ -155,19 +155,6 @@ struct HeadRotator {
     }
 };
 
-// A block takes kRotateWarps / parts tokens at a time: its threads make their cosines and
-// sines, one each, in shared memory, and each warp takes one token's heads (or one of `parts`
-// shares of them): LANES = D / 16 lanes a head, ROWS = 32 / LANES heads a step. A lane holds two
-// 16-byte chunks of a head whose values rotate with one another: chunks s and s + n/8 (halves),
-// or 2s and 2s + 1 (neighbours); either way its angles are those of frequencies 8s .. 8s + 7, the
-// same for every head of the token. The steps ahead, of the next token too, are on their way to
-// the lane's own places in shared memory, kRotateAhead of them: registers for as many would
-// leave too few warps.
-//
-// Bytes bound it: 16384 tokens of 64 + 8 heads of 128 with norms 98 us, 6.2 TB/s read and
-// written, 91% of the copy rate (two steps in registers instead: 117; a third block an SM, whose
-// registers spill: 125). 832 tokens of 28 + 4 + 4 heads into the cache 5.9 us, one token 2.2,
-// as much as an empty launch.
 // A lane's way through heads of one kind: its first chunk's address at the present step, and
 // how much further on the next step's is.
 struct HeadWalk {
@@ -189,6 +176,19 @@ struct HeadWalk {
     }
 };
 
+// A block takes kRotateWarps / parts tokens at a time: its threads make their cosines and
+// sines, one each, in shared memory, and each warp takes one token's heads (or one of `parts`
+// shares of them): LANES = D / 16 lanes a head, ROWS = 32 / LANES heads a step. A lane holds two
+// 16-byte chunks of a head whose values rotate with one another: chunks s and s + n/8 (halves),
+// or 2s and 2s + 1 (neighbours); either way its angles are those of frequencies 8s .. 8s + 7, the
+// same for every head of the token. The steps ahead, of the next token too, are on their way to
+// the lane's own places in shared memory, kRotateAhead of them: registers for as many would
+// leave too few warps.
+//
+// Bytes bound it: 16384 tokens of 64 + 8 heads of 128 with norms 98 us, 6.2 TB/s read and
+// written, 91% of the copy rate (two steps in registers instead: 117; a third block an SM, whose
+// registers spill: 125). 832 tokens of 28 + 4 + 4 heads into the cache 5.9 us, one token 1.9,
+// as much as an empty launch.
 template <int D, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kRotateThreads, kRotateBlocks)
     head_rotate_kernel(const HeadRotateArgs a) {

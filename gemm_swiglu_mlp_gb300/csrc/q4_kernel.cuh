@@ -13,7 +13,9 @@
 // code - 8 is exact; a group's products are summed as they are and the sum is
 // multiplied by the scale in FP32, so no weight is rounded. tcgen05 would take
 // the weights from shared or tensor memory, a write and a wait more for each of
-// them, to gain a rate that 16 tokens do not need.
+// them: up to 8 tokens its rate is not what is missing. From 9 on instructions bound
+// this kernel, and weights unpacked into tensor memory would take about half of them;
+// that form is not built.
 //
 // A CTA computes 128 columns of weights (the gated form: 64 output columns of both) for
 // up to 8 NT tokens over a share of K, in steps of 256 values of k. One warp loads a

@@ -17,17 +17,18 @@
 // and one of q are all there is to read, whatever the number of children.
 //
 // Sums are whole units of 2^-50 between lanes: with 32-bit sums (2^-24) one draw in
-// some hundreds would give a neighbour of the token. A lane adds its values up as pairs of FP32
-// numbers, each addition's error kept. The pairs' second numbers are rounded: at most 2^-43 of
-// the lane's sum for 16 values between two settlings, 2^-36 for the 2048 values that a
-// lane has of 2^20 over one CTA, and the lanes' own units 2^-37 and the draw's 2^-38 more, so
-// that a row's borders are held to 2^-35; rows of a softmax to about 2^-44, as roundings go
-// both ways (of a value .55 and 2^20 equal ones 2^-31 without settling). Conversions of every value to a 64-bit integer, which go at a rate of two a clock and
-// SM, were most of the time of a batch (64 rows of 128000 52 us), and digits taken
-// off by additions of constants half as many instructions again as the pairs.
+// some hundreds would give a neighbour of the token. A lane adds its values up as pairs of
+// FP32 numbers, each addition's error kept: conversions of every value to a 64-bit integer,
+// which go at a rate of two a clock and SM, were most of the time of a batch (64 rows of 128000
+// 52 us), and digits taken off by additions of constants half as many instructions again as
+// the pairs. The pairs' second numbers are rounded: by at most 2^-43 of the lane's sum for the
+// 16 values between two settlings, 2^-36 for the 2048 values that a lane has of 2^20 over one
+// CTA; the lanes' own units come to 2^-37 and the draw's to 2^-38 more. So a row's borders are
+// held to 2^-35, and those of a softmax's rows, whose roundings go both ways, to about
+// 2^-44 (without settling a row of .55 and 2^20 equal values was off by 2^-31).
 //
 // Measured (device time): 64 chains of 6 over 128000 values with a draft 17.5 us, of which the rows
-// that are read (45 MB) need 6.7 at the copy rate; 32 trees of 60 over 152000 without one 18.4
+// that are read (45 MB) need 6.7 at the copy rate; 32 trees of 60 over 152000 without one 18.1
 // (several rows one after the other); one chain of 5 over 32000 6.8; greedy 2.6. About 8 us are
 // the launch, three dependent loads before the walk (starts, tokens, their probabilities), the
 // exchange of the sums and the draw, each waiting for the one before.
