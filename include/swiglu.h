@@ -613,8 +613,9 @@ int swiglu_head_rotate_write(const void *q, int64_t q_token_stride, int64_t q_he
  * Probabilities are taken as they stand, clamped to [0, 1], NaN as 0; a row that sums to
  * more than 256 is no distribution, and its draw any of its tokens. Sums and borders are
  * held to 2^-35 of a row that sums to 1, and to about 2^-44 as a rule (a number nearer to a
- * border than that may fall to either side, and differently in a batch of another size); values below 2^-51 may count as 0, but the
- * token that follows always has some probability left, where any in its row counts.
+ * border than that may fall to either side, and differently in a batch of another size);
+ * values below 2^-51 may count as 0, but the token that follows always has some probability
+ * left, where the row's sum counts.
  * Outputs must not overlap each other or an input. tree_width 1 .. 4096, vocab up to
  * 2^20, requests < 2^27; requests = 0 is valid.
  * Errors: SWIGLU_ERR_INVALID_ARG, SWIGLU_ERR_UNSUPPORTED, SWIGLU_ERR_CUDA;
